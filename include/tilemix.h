@@ -511,6 +511,182 @@ typedef struct tilemix_mass_args {
  * the launch fails.  Argument errors return before any launch. */
 int tilemix_mass_probe(const tilemix_mass_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged 4-bit K/V cache.
+ *
+ * (The pages name lower-precision caches as an open direction and give no
+ * layout: these calls are this library's own.)  A pool of num_pages pages of
+ * page_size tokens; a page holds, per KV head and token, one row of K and one
+ * of V in 4 bits per channel with one scale per `group` channels:
+ *   a = max |x| over the group's channels, s = a / 7 rounded to the pool's
+ *   type, code = clamp(rne(x / s), -7, 7), stored as code + 8; the row stands
+ *   for code * s.  A group of zeros has s = 0; one that holds an infinity or a
+ *   NaN has s = NaN and codes 0 (it reads back as NaN).  Each row is coded by
+ *   itself, so a new token changes no row that is there.
+ *   k_codes, v_codes  [num_pages][hk][page_size][d / 2] bytes
+ *   k_scale, v_scale  [num_pages][hk][page_size][d / group], fp16 or bf16
+ * Order within a row of codes, low nibble first: K is stored in 32-bit words of
+ * 8 channels, word w (channels 8w .. 8w + 7) at place (w % 4) * (d / 32) + w / 4;
+ * V in 16-bit halfwords of 4 channels, halfword h (channels 4h .. 4h + 3) at
+ * place (h % 8) * (d / 32) + h / 8 (the operand order of the attention's
+ * matrix products).
+ * Sequence s keeps its token at position p in page block_table[s][p / page_size]
+ * at row p % page_size; its slot is page * page_size + row.  Pages may be in any
+ * order and may be shared by sequences that only read them. */
+enum { TILEMIX_KV_FP16 = 0, TILEMIX_KV_BF16 = 1 };
+typedef struct tilemix_kv4_cache {
+  uint8_t* k_codes;           /* device, 16-byte aligned, and so the next three */
+  void* k_scale;
+  uint8_t* v_codes;
+  void* v_scale;
+  int num_pages;              /* >= 1; num_pages * page_size < 2^31 */
+  int page_size;              /* a power of two, 16 .. 1024 */
+  int hk, d;                  /* d in {64, 128} */
+  int group;                  /* 32, 64 or 128, at most d */
+  int dtype;                  /* TILEMIX_KV_FP16 or TILEMIX_KV_BF16: the type of the scales
+                                 and of every q, k, v and o of these calls */
+} tilemix_kv4_cache;
+
+/* Most sequences of one tilemix_page_plan call. */
+#define TILEMIX_PAGE_PLAN_MAX_SEQS 8192
+
+/* Block tables and slot maps of one step, built on the device from the
+ * requests' lengths.  For sequence s with L = seq_len[s] tokens:
+ *   new_len[s] = n > 0   n tokens are added at positions L .. L + n - 1; pages
+ *                        for ceil((L + n) / page_size) - ceil(L / page_size)
+ *                        table entries are taken from the free stack
+ *   new_len[s] = 0       nothing changes
+ *   new_len[s] = -n < 0  the last min(n, L) tokens are dropped (a rejected draft;
+ *                        n >= L ends the request); pages that hold none of the
+ *                        remaining tokens go back and their entries become -1
+ * The tokens added are numbered in sequence order: token_start[s] = the sum of
+ * the positive new_len before s (token_start[nseq]: all of them; a sum past
+ * 2^31 - 1 reads as 2^31 - 1), and slots[token_start[s] + i] is the slot of position
+ * L + i.  Returned pages go back before any is taken.  With F free pages and R
+ * returned ones, the k-th returned page (sequences ascending, entries
+ * ascending) goes to free_list[F + R - 1 - k] and the k-th page taken is
+ * free_list[F + R - 1 - k]: the free stack grows at its end, and a step that is
+ * dropped again leaves it as it was.  A sequence's tokens fit if token_start[s + 1]
+ * <= max_tokens and ceil((L + n) / page_size) <= max_pages; in sequence order,
+ * tokens that fit are granted while the pages needed so far (granted or not,
+ * of those that fit) do not exceed F + R, or if they need none.  Tokens that are
+ * not granted leave their sequence as it was: granted[s] = 0, their slots -1.
+ * Everything else has granted[s] = 1.  Slots past the last token are -1.
+ * Integer arithmetic in a fixed order: the same inputs give the same tables.
+ * One launch.  Tables that contradict themselves (a length outside
+ * [0, max_pages * page_size], a free count outside [0, num_pages], an entry or a
+ * stack that names no page) are never followed out of the arrays; they are
+ * reported by tilemix_get_error() as INVALID_ARG and the affected entries are
+ * then meaningless. */
+typedef struct tilemix_page_plan_args {
+  const int32_t* new_len;     /* device [nseq] */
+  int32_t* seq_len;           /* device [nseq], updated */
+  int32_t* block_table;       /* device [nseq][max_pages], updated */
+  int32_t* free_list;         /* device [num_pages], updated: a stack of page numbers */
+  int32_t* free_count;        /* device [1], updated: its height */
+  int32_t* token_start;       /* device [nseq + 1] out */
+  int32_t* slots;             /* device [max_tokens] out (NULL if max_tokens is 0) */
+  int32_t* granted;           /* device [nseq] out */
+  int nseq;                   /* 0 .. TILEMIX_PAGE_PLAN_MAX_SEQS */
+  int max_pages;              /* entries of a block-table row, >= 1 */
+  int num_pages, page_size;   /* as in tilemix_kv4_cache */
+  int max_tokens;             /* entries of slots, >= 0 */
+} tilemix_page_plan_args;
+
+/* INVALID_ARG on a NULL pointer or a size out of range, UNSUPPORTED for a
+ * page_size that is no power of two in 16 .. 1024 or too many sequences, CUDA
+ * if the launch fails; all before anything is enqueued. */
+int tilemix_page_plan(const tilemix_page_plan_args* args, void* stream);
+
+/* Rows into the cache: token t's K and V of every KV head are coded and written
+ * to slot slots[t].  A slot of -1 is skipped (a token without a place, or
+ * padding); any other slot outside the pool is skipped and reported by
+ * tilemix_get_error() as INVALID_ARG.  Slots other than -1 must be distinct: of
+ * two tokens with the same slot, which one each part of the row then holds is
+ * not defined.  One launch. */
+typedef struct tilemix_kv4_append_args {
+  tilemix_kv4_cache cache;
+  const void* k;              /* device [n][hk][d] of the cache's type, 16-byte aligned */
+  const void* v;
+  int64_t k_stride;           /* elements from one token to the next: >= hk * d, a */
+  int64_t v_stride;           /* multiple of 8 (K and V may lie in one wider tensor) */
+  const int32_t* slots;       /* device [n] */
+  int n;                      /* tokens, >= 0; n * hk * d / 8 < 2^31 */
+} tilemix_kv4_append_args;
+
+/* INVALID_ARG on a NULL or misaligned pointer, a bad stride or a size out of
+ * range, UNSUPPORTED for a d, group, page_size or
+ * dtype that is not built, CUDA if the launch fails. */
+int tilemix_kv4_append(const tilemix_kv4_append_args* args, void* stream);
+
+/* Rows out of the cache: positions 0 .. seq_len[s] - 1 of sequence s to rows
+ * out_start[s] + position of k and v, as code * s rounded once to the cache's
+ * type.  Rows outside [0, rows) are skipped and reported by tilemix_get_error()
+ * as INVALID_ARG, and so are positions whose table entry names no page.  Rows
+ * that no sequence covers are left as they were.  One launch. */
+typedef struct tilemix_kv4_gather_args {
+  tilemix_kv4_cache cache;
+  const int32_t* block_table; /* device [nseq][max_pages] */
+  const int32_t* seq_len;     /* device [nseq], each at most max_pages * page_size */
+  const int32_t* out_start;   /* device [nseq] */
+  void* k;                    /* device out [rows][hk][d], 16-byte aligned */
+  void* v;
+  int nseq;                   /* 0 .. 65535 */
+  int max_pages;              /* >= 1 */
+  int rows;                   /* >= 0 */
+} tilemix_kv4_gather_args;
+int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
+
+/* Attention of new tokens over the cache.  Sequence s has seq_len[s] tokens in
+ * the cache, the new ones last (appended before this call), and its queries are
+ * rows token_start[s] .. token_start[s + 1] - 1 of q: n of them, the i-th at
+ * position seq_len[s] - n + i, attending to the positions up to its own.
+ *   O = softmax(scale * q . K^T) V over the values the codes stand for;
+ *   scores, softmax and O's sums in fp32 (the codes are exact operands of the
+ *   matrix products, q is used to at least 11 bits below its row's largest
+ *   magnitude, each probability times its V scale is rounded once to 11 bits),
+ *   O rounded once to the cache's type.
+ * A query with no position to attend to gets O = 0 and an LSE of -infinity.  A
+ * sequence with no queries reads nothing.  Rows of q and o at and behind
+ * token_start[nseq] are not touched.  One launch; results do not depend on
+ * timing (partial results are combined in a fixed order).
+ * Queries are taken in blocks of 8 (or 16, if max_new * hq / hk > 8) columns, a
+ * column being one query token of one of the hq / hk heads that share a KV head; each
+ * block reads its sequence's cached rows once. */
+#define TILEMIX_KV4_SYNC_WORDS 1024
+typedef struct tilemix_kv4_attn_args {
+  tilemix_kv4_cache cache;
+  const void* q;              /* device [total_q][hq][d], 16-byte aligned */
+  void* o;                    /* device out, like q */
+  float* lse;                 /* device out fp32 [hq][total_q] natural-log LSE, or NULL */
+  const int32_t* token_start; /* device [nseq + 1], or NULL: one query per sequence,
+                                 row s (then total_q >= nseq) */
+  const int32_t* seq_len;     /* device [nseq], each at most max_pages * page_size */
+  const int32_t* block_table; /* device [nseq][max_pages] */
+  int nseq;                   /* >= 0 */
+  int total_q;                /* rows of q and o, >= 0 */
+  int max_new;                /* most queries of a sequence, >= 1: picks the column block,
+                                 a smaller value than the true one costs only time */
+  int max_seqlen;             /* longest sequence, >= 1: sizes the grid, likewise */
+  int max_pages;              /* >= 1 */
+  int hq;                     /* hq % hk == 0 */
+  float softmax_scale;        /* 0 => 1 / sqrt(d) */
+  void* workspace;            /* device, >= tilemix_kv4_attn_workspace_size(), 256-aligned */
+  size_t workspace_bytes;
+  uint32_t* sync;             /* device [TILEMIX_KV4_SYNC_WORDS]: zero before the first call
+                                 that uses it; every call leaves it zero.  Calls that may
+                                 run at the same time need a workspace and a sync array
+                                 each */
+} tilemix_kv4_attn_args;
+
+/* Bytes of workspace (partial softmax states; about 12 MB on a B200, whatever the batch). */
+int tilemix_kv4_attn_workspace_size(const tilemix_kv4_attn_args* args, size_t* bytes);
+
+/* INVALID_ARG on a NULL or misaligned pointer, a size out of range or hq % hk != 0;
+ * UNSUPPORTED for a d, group, page_size or dtype that is not built; WORKSPACE if
+ * the workspace is missing, misaligned or too small; CUDA if the launch fails. */
+int tilemix_kv4_attn(const tilemix_kv4_attn_args* args, void* stream);
+
 /* Self test of the failure path: enqueues one warp that waits on a device
  * barrier nothing ever signals, with the same bounded wait the attention
  * kernel uses, limited to timeout_ms (1..10000).  The wait gives up, latches
@@ -536,8 +712,9 @@ int tilemix_mma_rate(int form, int n, int iters, int ctas, long long* cycles_dev
 
 /* Synchronises `stream`, then returns and clears the device status word:
  * OK, TIMEOUT (a bounded wait expired), INVALID_ARG (a row needed more than 64
- * groups, a bad routing-group factor, or a head-map entry outside [0, hk): the
- * work items concerned are skipped), or CUDA for a sticky CUDA error. */
+ * groups, a bad routing-group factor, a head-map entry outside [0, hk), or a page,
+ * slot or row of a paged-cache call outside its array: the work items concerned
+ * are skipped), or CUDA for a sticky CUDA error. */
 int tilemix_get_error(void* stream);
 
 #ifdef __cplusplus

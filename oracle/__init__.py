@@ -13,7 +13,7 @@ own splitmix64), and plain C in fp64 / int64 for the attention rows
 (content-aware) routing policy in fp32 in its stated order; ``mass.py`` is the
 fp64 importance-mass exposure probe; ``fp8.py`` the e4m3 codec and block
 quantiser of the FP8 low path (the C attention oracle reads those codes when
-asked to).  It shares no code,
+asked to), ``kv4.py`` the paged 4-bit K/V cache (numpy in fp64, and host lists).  It shares no code,
 header, table or constant generator with the CUDA path.
 
 Pages followed: "TileMix: Tile-Centric Mixed-Precision Attention for LLM
@@ -31,7 +31,7 @@ routed scores key by key for mixed and all-INT8 words) on small batches.  The
 pages print no worked numeric example of an output, so no stored expected
 output value comes from the pages.
 """
-from . import adaptive, fp8, mass
+from . import adaptive, fp8, kv4, mass
 from .attention import all_rows, attention_rows, build, half_to_double, int_scores
 from .decode import decode_rows, quantize_rows
 from .quant import quantize_blocks, quantize_k, quantize_k_int4, quantize_q, quantize_q_int4
@@ -40,7 +40,7 @@ from .routing import (BLOCK_M, BLOCK_N, MAX_GROUPS, TEMPLATES, auto_g, build_rou
                       n_qtiles, tile_offsets)
 
 __all__ = [
-    "adaptive", "fp8", "mass", "BLOCK_M", "BLOCK_N", "MAX_GROUPS", "TEMPLATES", "all_rows", "attention_rows", "auto_g",
+    "adaptive", "fp8", "kv4", "mass", "BLOCK_M", "BLOCK_N", "MAX_GROUPS", "TEMPLATES", "all_rows", "attention_rows", "auto_g",
     "build", "build_routing", "decode_rows", "fp16_groups", "half_to_double", "int8_target",
     "int_scores",
     "last_legal_tile", "legal_groups", "n_ktiles", "n_qtiles", "quantize_blocks",

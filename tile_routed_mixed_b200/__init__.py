@@ -99,6 +99,65 @@ class RouteArgs(ctypes.Structure):
     ]
 
 
+KV_DTYPES = {"fp16": 0, "bf16": 1}
+KV4_SYNC_WORDS = 1024
+PAGE_PLAN_MAX_SEQS = 8192
+
+
+class KV4Cache(ctypes.Structure):
+    """Mirror of ``tilemix_kv4_cache``."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_codes", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("hk", ctypes.c_int), ("d", ctypes.c_int), ("group", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
+class PagePlanArgs(ctypes.Structure):
+    """Mirror of ``tilemix_page_plan_args``."""
+    _fields_ = [
+        ("new_len", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("free_list", ctypes.c_void_p),
+        ("free_count", ctypes.c_void_p), ("token_start", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p), ("granted", ctypes.c_void_p),
+        ("nseq", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("max_tokens", ctypes.c_int),
+    ]
+
+
+class KV4AppendArgs(ctypes.Structure):
+    """Mirror of ``tilemix_kv4_append_args``."""
+    _fields_ = [
+        ("cache", KV4Cache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("n", ctypes.c_int),
+    ]
+
+
+class KV4GatherArgs(ctypes.Structure):
+    """Mirror of ``tilemix_kv4_gather_args``."""
+    _fields_ = [
+        ("cache", KV4Cache), ("block_table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+        ("out_start", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("nseq", ctypes.c_int), ("max_pages", ctypes.c_int), ("rows", ctypes.c_int),
+    ]
+
+
+class KV4AttnArgs(ctypes.Structure):
+    """Mirror of ``tilemix_kv4_attn_args``."""
+    _fields_ = [
+        ("cache", KV4Cache), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("token_start", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("nseq", ctypes.c_int), ("total_q", ctypes.c_int), ("max_new", ctypes.c_int),
+        ("max_seqlen", ctypes.c_int), ("max_pages", ctypes.c_int), ("hq", ctypes.c_int),
+        ("softmax_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("sync", ctypes.c_void_p),
+    ]
+
+
 class MassArgs(ctypes.Structure):
     """Mirror of ``tilemix_mass_args``."""
     _fields_ = [
@@ -167,6 +226,17 @@ def lib():
         L.tilemix_route_pooled.argtypes = [ctypes.POINTER(RouteArgs), P]
         L.tilemix_mass_probe.restype = I
         L.tilemix_mass_probe.argtypes = [ctypes.POINTER(MassArgs), P]
+        L.tilemix_page_plan.restype = I
+        L.tilemix_page_plan.argtypes = [ctypes.POINTER(PagePlanArgs), P]
+        L.tilemix_kv4_append.restype = I
+        L.tilemix_kv4_append.argtypes = [ctypes.POINTER(KV4AppendArgs), P]
+        L.tilemix_kv4_gather.restype = I
+        L.tilemix_kv4_gather.argtypes = [ctypes.POINTER(KV4GatherArgs), P]
+        L.tilemix_kv4_attn_workspace_size.restype = I
+        L.tilemix_kv4_attn_workspace_size.argtypes = [ctypes.POINTER(KV4AttnArgs),
+                                                      ctypes.POINTER(ctypes.c_size_t)]
+        L.tilemix_kv4_attn.restype = I
+        L.tilemix_kv4_attn.argtypes = [ctypes.POINTER(KV4AttnArgs), P]
         L.tilemix_selftest_wait_timeout.restype = I
         L.tilemix_selftest_wait_timeout.argtypes = [I, P]
         L.tilemix_get_error.restype = I
@@ -506,8 +576,36 @@ def mass_probe(q, k, masks, lengths, hq, hk, g, causal=True, delta_log2=4.0, kv_
     return tuple(out)
 
 
+def tilemix_page_plan(args: PagePlanArgs, stream=None):
+    _check(lib().tilemix_page_plan(ctypes.byref(args), _stream_handle(stream)),
+           "tilemix_page_plan")
+
+
+def tilemix_kv4_append(args: KV4AppendArgs, stream=None):
+    _check(lib().tilemix_kv4_append(ctypes.byref(args), _stream_handle(stream)),
+           "tilemix_kv4_append")
+
+
+def tilemix_kv4_gather(args: KV4GatherArgs, stream=None):
+    _check(lib().tilemix_kv4_gather(ctypes.byref(args), _stream_handle(stream)),
+           "tilemix_kv4_gather")
+
+
+def tilemix_kv4_attn_workspace_size(args: KV4AttnArgs) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().tilemix_kv4_attn_workspace_size(ctypes.byref(args), ctypes.byref(n)),
+           "tilemix_kv4_attn_workspace_size")
+    return int(n.value)
+
+
+def tilemix_kv4_attn(args: KV4AttnArgs, stream=None):
+    _check(lib().tilemix_kv4_attn(ctypes.byref(args), _stream_handle(stream)),
+           "tilemix_kv4_attn")
+
+
 from .prefill import TileMixPrefill  # noqa: E402  (convenience wrapper)
 from .decode import TileMixDecode  # noqa: E402  (convenience wrapper)
+from .kv4 import PagePlan, TileMixKV4Cache  # noqa: E402  (convenience wrapper)
 
 __all__ = [
     "BLOCK_M", "BLOCK_N", "DecodeArgs", "MAX_GROUPS", "PrefillArgs", "RouteArgs", "TEMPLATES",
@@ -521,4 +619,8 @@ __all__ = [
     "PrefillHostArgs", "tilemix_prefill_host", "tilemix_host_runs",
     "tilemix_status_string", "tilemix_tile_offsets", "tilemix_version",
     "tilemix_workspace_size", "tilemix_mma_rate", "mma_rate",
+    "KV_DTYPES", "KV4AppendArgs", "KV4AttnArgs", "KV4Cache", "KV4GatherArgs", "KV4_SYNC_WORDS",
+    "PAGE_PLAN_MAX_SEQS", "PagePlan", "PagePlanArgs", "TileMixKV4Cache", "tilemix_kv4_append",
+    "tilemix_kv4_attn", "tilemix_kv4_attn_workspace_size", "tilemix_kv4_gather",
+    "tilemix_page_plan",
 ]

@@ -10,9 +10,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtilemix.so")
 SOURCES = ["tilemix_kernels.cu", "tilemix_quantize.cu", "tilemix_route.cu", "tilemix_mass.cu",
-           "tilemix_mmarate.cu", "api.cpp", "routing.cpp"]
+           "tilemix_mmarate.cu", "tilemix_kv4.cu", "api.cpp", "kv4_api.cpp", "routing.cpp"]
 HEADERS = ["tilemix_internal.h", "tilemix_ptx.cuh", "tilemix_quant.cuh", "tilemix_decode.cuh",
-           "tilemix_mma.cuh"]
+           "tilemix_mma.cuh", "tilemix_kv4.h", "tilemix_kv4_plan.cuh", "tilemix_kv4_rows.cuh",
+           "tilemix_kv4_attn.cuh"]
 NVCC_FLAGS = [
     "-std=c++17", "-O3", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -12,6 +12,7 @@
 
 #include "tilemix.h"
 #include "tilemix_internal.h"
+#include "tilemix_kv4.h"
 
 namespace {
 
@@ -714,8 +715,11 @@ TILEMIX_API int tilemix_get_error(void* stream) {
   unsigned int status = 0;
   if (tilemix::read_and_clear_status(&status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return TILEMIX_ERR_CUDA;
+  unsigned int kv4 = 0;
+  if (tilemix::kv4_read_and_clear_status(&kv4) != cudaSuccess) return TILEMIX_ERR_CUDA;
+  status |= kv4;
   if (status & tilemix::kStatusTimeout) return TILEMIX_ERR_TIMEOUT;
-  if (status & (tilemix::kStatusBadGroups | tilemix::kStatusBadHeadMap))
+  if (status & (tilemix::kStatusBadGroups | tilemix::kStatusBadHeadMap | tilemix::kStatusBadPages))
     return TILEMIX_ERR_INVALID_ARG;
   return TILEMIX_OK;
 }

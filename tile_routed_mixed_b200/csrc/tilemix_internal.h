@@ -15,6 +15,7 @@ enum : unsigned int {
   kStatusTimeout = 1u,       // a bounded mbarrier wait expired
   kStatusBadGroups = 2u,     // a row needed a routing group index above 63
   kStatusBadHeadMap = 4u,    // a head-map entry outside [0, hk)
+  kStatusBadPages = 8u,      // a page, slot or row of the paged cache outside its array
 };
 
 

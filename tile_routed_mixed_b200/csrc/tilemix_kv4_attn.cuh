@@ -1,0 +1,825 @@
+// Attention over the paged 4-bit cache (tilemix_kv4_attn).
+//
+// A unit of work is one (sequence, KV head, block of columns); a column is one
+// query token of one of the KV head's query heads, and a block has 8 NB of
+// them.  A unit's keys are cut into tiles of 32.  All tiles of all units, in
+// order, are dealt out in equal contiguous ranges to the warps of the grid, so
+// the split over a long axis and the balance of a ragged batch are the same
+// thing.  A warp works alone: it streams its tiles through a ring of its own
+// in shared memory (cp.async), with its own running maximum, sum and output,
+// and meets the other warps of its CTA only once, at the end.
+//
+// Products.  The step reads each cached byte once and is bound by HBM as long
+// as a tile's arithmetic stays under its transfer time, about 180 cycles of an
+// SM for the 4.2 KB of a tile.  What has to be short is the way from 4 bits to
+// an operand of the matrix product:
+//   - codes are stored as u = code + 8, and a nibble in the top four of an
+//     fp16's ten significand bits, exponent field 0, is the subnormal u 2^-18,
+//     an exact operand as it stands: a shift and an AND per pair of codes, no
+//     conversion, no subtraction.  (At bits 0 and 4 two of the four shifts fall
+//     away, but the products are aligned by the subnormals' exponent, 2^-14, not
+//     by their leading bit, before they are added: sums then lose six more
+//     bits, measured as errors of 1e-4 of a code.);
+//   - keys are the rows (M = 16) of both products, queries the 8 columns, so
+//     that no row is padding: S^T = K Q^T, and O^T = V^T P^T;
+//   - the offset 8 leaves as 8 sum(q) per column from each score and as
+//     8 sum(P) per column from each output; sum(P) comes from a product with
+//     ones, in the layout of the outputs.
+// Q is scaled per column by a power of two, so its largest magnitude is near
+// 2^14 and every channel keeps at least 11 bits (fp16 has 5 of exponent,
+// bf16 has 8) down to 2^-28 of it.  K's scales multiply the scores, V's the
+// probabilities: P s_v, over a running power of two near the largest V
+// scale, is what is rounded to fp16.  The running maximum moves only when a
+// score passes it by 2^8: P s_v stays below 2^14, and fp32 holds the sums.
+//
+// Layouts.  With MMA fragments (rows g and g + 8, column pairs q4) a lane's
+// operands of K are D / 32 words of a key's row, 16 (or 8) bytes together in
+// the pool's order, and those of V 8 (or 4) bytes of four keys.  Row r of a
+// block of 16 is key r ^ ((r >> 1) & 1): the four keys that a quarter of the
+// lanes reads from V, and the two that eight lanes read from K, then fall
+// into different banks (with V's 16-byte chunks exchanged by bit 2 of the key).
+// Included by tilemix_kv4.cu.
+#pragma once
+
+namespace tilemix {
+
+constexpr int kAttnWarps = 8;
+constexpr int kAttnThreads = 32 * kAttnWarps;
+constexpr int kAttnKeys = 32;      // keys of a tile
+constexpr int kAttnMinTiles = 16;  // tiles a CTA takes at least, while there are any
+
+template <int D, int GROUP>
+struct AttnTile {
+  static constexpr int kNg = D / GROUP;                 // scales per row
+  static constexpr int kT = D / 32;                     // 32-channel chunks of a row
+  static constexpr int kCodes = kAttnKeys * D / 2;      // bytes of K's (and V's) codes
+  static constexpr int kScales = kAttnKeys * 2 * kNg;   // ... and scales
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kOffV = kCodes;
+  static constexpr int kOffKs = 2 * kCodes;
+  static constexpr int kOffVs = 2 * kCodes + kScales;
+  // as many stages as fit beside the merge's weights, at most six
+  static constexpr int kStages = 200 * 1024 / (kAttnWarps * kBytes) > 6
+                                     ? 6
+                                     : 200 * 1024 / (kAttnWarps * kBytes);
+  static_assert(kStages >= 3, "ring too short");
+};
+
+namespace kv4 {
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Nibble I of both halves of x as two fp16 subnormals u 2^-18.
+template <int I>
+__device__ __forceinline__ uint32_t nibble(uint32_t x) {
+  constexpr int by = 6 - 4 * I;
+  return (by >= 0 ? x << (by >= 0 ? by : 0) : x >> (by < 0 ? -by : 0)) & 0x03C003C0u;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ float max_over_rows(float x) {  // over the lanes of a column pair
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// What the schedule needs to know about a sequence.
+struct SeqWork {
+  int len, queries, row0;  // keys, query tokens, first row of q
+  int blocks, tiles;       // column blocks, key tiles of a unit
+};
+template <int NB>
+__device__ __forceinline__ SeqWork seq_work(const Kv4AttnParams& p, int s) {
+  SeqWork w;
+  const long long top = min(static_cast<long long>(p.max_pages) << p.pool.page_shift, 0x7fffff00LL);
+  const int have = __ldg(p.seq_len + s);
+  w.len = static_cast<int>(min(static_cast<long long>(max(have, 0)), top));
+  w.row0 = s;
+  w.queries = 1;
+  if (p.token_start) {
+    w.row0 = __ldg(p.token_start + s);
+    const long long n = static_cast<long long>(__ldg(p.token_start + s + 1)) - w.row0;
+    w.queries = static_cast<int>(min(max(n, 0LL), static_cast<long long>(p.total_q)));
+  }
+  w.blocks = static_cast<int>((static_cast<unsigned>(w.queries) * p.group_q + 8 * NB - 1) / (8 * NB));
+  w.tiles = max(1, (w.len + kAttnKeys - 1) / kAttnKeys);
+  return w;
+}
+__device__ __forceinline__ long long seq_tiles(const Kv4AttnParams& p, const SeqWork& w) {
+  return static_cast<long long>(p.pool.hk) * w.blocks * w.tiles;
+}
+
+// Column `col` of a unit's block: its row of q and its query head; false for
+// padding (and for rows outside q).
+template <int NB>
+__device__ __forceinline__ bool column(const Kv4AttnParams& p, const SeqWork& w, int kv, int block,
+                                       int col, int* token, int* row, int* head) {
+  const unsigned c = block * (8u * NB) + col;
+  const unsigned tok = c / p.group_q;
+  *token = static_cast<int>(tok);
+  *head = kv * p.group_q + static_cast<int>(c - tok * p.group_q);
+  *row = w.row0 + *token;
+  return *token < w.queries && *row >= 0 && *row < p.total_q;
+}
+
+// A place in the list of all tiles: tile t of unit u of sequence s.
+template <int NB>
+struct Cursor {
+  int s, u, t;
+  SeqWork w;
+  int kv, block;
+  int keys;  // keys that some column of the unit may see
+  __device__ __forceinline__ void enter_unit(const Kv4AttnParams& p) {
+    kv = u / w.blocks;
+    block = u - kv * w.blocks;
+    // total_q * hq < 2^31, so columns fit an unsigned int
+    const int last = min(static_cast<int>((block * (8u * NB) + 8u * NB - 1) / p.group_q), w.queries - 1);
+    keys = max(0, w.len - w.queries + last + 1);
+  }
+  __device__ __forceinline__ void start(const Kv4AttnParams& p, int seq, long long off) {
+    s = seq;
+    w = seq_work<NB>(p, s);
+    u = static_cast<int>(off / w.tiles);
+    t = static_cast<int>(off - static_cast<long long>(u) * w.tiles);
+    enter_unit(p);
+  }
+  // To the first tile of the next unit; false past the last one.
+  __device__ __forceinline__ bool next_unit(const Kv4AttnParams& p) {
+    t = 0;
+    if (++u == p.pool.hk * w.blocks) {
+      u = 0;
+      do {
+        if (++s >= p.nseq) return false;
+        w = seq_work<NB>(p, s);
+      } while (w.blocks == 0);
+    }
+    enter_unit(p);
+    return true;
+  }
+};
+
+// A partial state (maximum, sum and unnormalised output of every column of a
+// unit): [columns][D] outputs, then [columns] maxima, then [columns] sums.
+template <int D, int NB>
+constexpr int kPartFloats = 8 * NB * (D + 2);
+
+struct Part {
+  long long first;  // the unit's first tile in the list of all tiles
+  int s, kv, block, tiles;
+  float* at;        // nullptr: none
+};
+
+}  // namespace kv4
+
+template <int D, int GROUP, int NB, bool BF16>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
+  using Tile = AttnTile<D, GROUP>;
+  constexpr int kNg = Tile::kNg, kT = Tile::kT, kStages = Tile::kStages;
+  constexpr int kCols = 8 * NB;
+  constexpr int kTg = kT / kNg;  // chunks per scale group
+  extern __shared__ __align__(128) uint8_t attn_smem[];
+  __shared__ long long warp_tiles[kAttnWarps];
+  __shared__ int start_seq[kAttnWarps];
+  __shared__ long long start_off[kAttnWarps];
+  __shared__ kv4::Part parts[2 * kAttnWarps];
+  __shared__ float* run[2 * kAttnWarps];
+  __shared__ float top[kCols], sum[kCols];
+  __shared__ int merge_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, q4 = lane & 3;
+
+  // ---- the schedule: this CTA's tiles [a, b), this warp's [wa, wb) ----
+  const int per = (p.nseq + kAttnThreads - 1) / kAttnThreads;
+  const int s0 = min(p.nseq, tid * per), s1 = min(p.nseq, s0 + per);
+  long long mine = 0;
+  for (int s = s0; s < s1; ++s) mine += kv4::seq_tiles(p, kv4::seq_work<NB>(p, s));
+  long long inc = mine;
+#pragma unroll
+  for (int by = 1; by < 32; by <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, inc, by);
+    if (lane >= by) inc += up;
+  }
+  if (lane == 31) warp_tiles[warp] = inc;
+  if (tid < 2 * kAttnWarps) parts[tid].at = nullptr;
+  __syncthreads();
+  long long base = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kAttnWarps; ++w) {
+    if (w < warp) base += warp_tiles[w];
+    total += warp_tiles[w];
+  }
+  const long long most = (total + kAttnMinTiles - 1) / kAttnMinTiles;
+  const long long ctas = most < gridDim.x ? most : gridDim.x;
+  if (static_cast<long long>(blockIdx.x) >= ctas) return;
+  const long long a = blockIdx.x * total / ctas, b = (blockIdx.x + 1) * total / ctas;
+  const auto warp_begin = [&](int w) { return a + (b - a) * w / kAttnWarps; };
+#pragma unroll 1
+  for (int w = 0; w < kAttnWarps; ++w) {
+    const long long x = warp_begin(w);
+    if (x >= base && x < base + mine) {
+      long long off = x - base;
+      int s = s0;
+      for (;; ++s) {
+        const long long n = kv4::seq_tiles(p, kv4::seq_work<NB>(p, s));
+        if (off < n || s + 1 >= s1) break;
+        off -= n;
+      }
+      start_seq[w] = s;
+      start_off[w] = off;
+    }
+  }
+  __syncthreads();
+  const long long wa = warp_begin(warp), wb = warp_begin(warp + 1);
+
+  // ---- this warp's tiles ----
+  if (wa < wb) {
+    uint8_t* ring = attn_smem + warp * (kStages * Tile::kBytes);
+    const uint32_t ring_addr = ptx::smem_addr(ring);
+    kv4::Cursor<NB> in;  // the next tile to fetch
+    in.start(p, start_seq[warp], start_off[warp]);
+    kv4::Cursor<NB> cur = in;
+    long long to_issue = wb - wa;
+    const int page_sh = p.pool.page_shift, page_1 = (1 << page_sh) - 1;
+
+    // Fetches tile `in` into `stage` and moves on.  Keys come in two halves of
+    // 16, each within one page; a half that no column sees is not fetched.
+    const auto issue = [&](int stage) {
+      if (to_issue > 0) {
+        --to_issue;
+        const int key0 = in.t * kAttnKeys;
+        if (key0 < in.keys) {
+          const int32_t* table = p.block_table + static_cast<size_t>(in.s) * p.max_pages;
+          const uint32_t dst = ring_addr + stage * Tile::kBytes;
+          size_t row[2];
+          bool on[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = key0 + 16 * h;
+            on[h] = key < in.keys;
+            const int page = on[h] ? __ldg(table + (key >> page_sh)) : 0;
+            if (page < 0 || page >= p.pool.num_pages) {
+              on[h] = false;
+              atomicOr(&g_kv4_status, kStatusBadPages);
+            }
+            row[h] = ((static_cast<size_t>(page) * p.pool.hk + in.kv) << page_sh) + (key & page_1);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (on[h]) {
+              const uint8_t* ks = p.pool.k_codes + row[h] * (D / 2);
+              const uint8_t* vs = p.pool.v_codes + row[h] * (D / 2);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i) {
+                const int c = lane + 32 * i;  // 16-byte chunk of the half
+                const uint32_t at = dst + h * (8 * D);
+                kv4::cp16(at + c * 16, ks + c * 16);
+                // V: chunks of a 64-byte row exchanged by bit 2 of the key
+                const int sw = D == 128 ? ((c >> 4) & 1) << 5 : 0;
+                kv4::cp16(at + Tile::kOffV + ((c * 16) ^ sw), vs + c * 16);
+              }
+            }
+          }
+          // scales: 2 kNg chunks for each half of K and of V
+          if (lane < 8 * kNg) {
+            const int c = lane % (2 * kNg), h = (lane / (2 * kNg)) & 1, v = lane / (4 * kNg);
+            const uint8_t* src = (v ? p.pool.v_scale : p.pool.k_scale) +
+                                 (h ? row[1] : row[0]) * (2 * kNg) + c * 16;
+            if (h ? on[1] : on[0])
+              kv4::cp16(dst + Tile::kOffKs + v * Tile::kScales + h * (32 * kNg) + c * 16, src);
+          }
+        }
+        if (++in.t == in.w.tiles && to_issue > 0 && !in.next_unit(p)) to_issue = 0;
+      }
+      kv4::cp_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    int stage = 0;
+    long long left = wb - wa;
+    long long unit_first = wa - cur.t;
+    // rows of a block of 16 that this lane reads: keys of rows g, 2 q4, 2 q4 + 1
+    const int key_g = g ^ ((g >> 1) & 1);
+    const int key_e0 = (2 * q4) ^ (q4 & 1), key_e1 = (2 * q4 + 1) ^ (q4 & 1);
+    const int v_sw = D == 128 ? (((g >> 1) ^ ((q4 >> 1) << 1)) << 4) + (g & 1) * 8 : g * 4;
+
+#pragma unroll 1
+    while (left > 0) {
+      // ---- a unit: its queries ----
+      const int n = static_cast<int>(min(left, static_cast<long long>(cur.w.tiles - cur.t)));
+      const bool whole = cur.t == 0 && n == cur.w.tiles;
+      const bool head = !whole && n < left;  // more tiles of this warp follow
+      uint32_t qf[NB][kT][4];
+      float cs[NB][2], corr[NB][2][kNg];
+      int lim[NB][2];  // keys that each column sees
+      const int seen0 = cur.w.len - cur.w.queries + 1;  // ... of query token 0
+      const int min_lim =
+          min(seen0 + static_cast<int>(static_cast<unsigned>(cur.block) * kCols / p.group_q), cur.w.len);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        int tok, row, hq;
+        const bool on = kv4::column<NB>(p, cur.w, cur.kv, cur.block, 8 * nb + g, &tok, &row, &hq);
+        const uint8_t* src = p.q + (static_cast<size_t>(on ? row : 0) * p.hq + (on ? hq : 0)) * (2 * D);
+        uint4 x[kT];
+        uint32_t am = 0;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          x[t] = make_uint4(0u, 0u, 0u, 0u);
+          if (on) x[t] = __ldg(reinterpret_cast<const uint4*>(src + 16 * (4 * t + q4)));
+          am = max(am, kv4::absmax_bits(x[t]));
+        }
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+        am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+        // f = 2^(14 - exponent of the largest magnitude), 1 for zeros, infinities, NaN
+        const uint32_t ex = __float_as_uint(kv4::unpack1<BF16>(am)) >> 23;
+        const uint32_t fe = (am == 0 || am >= kv4::kInfBits<BF16>) ? 127u : min(268u - ex, 253u);
+        const float f = __uint_as_float(fe << 23);
+        const float inv_f = __uint_as_float((254u - fe) << 23);
+        float sums[kNg];
+#pragma unroll
+        for (int i = 0; i < kNg; ++i) sums[i] = 0.f;
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          const float2 c01 = kv4::unpack2<BF16>(x[t].x), c23 = kv4::unpack2<BF16>(x[t].y);
+          const float2 c45 = kv4::unpack2<BF16>(x[t].z), c67 = kv4::unpack2<BF16>(x[t].w);
+          qf[nb][t][0] = kv4::pack2<false>(c01.x * f, c45.x * f);
+          qf[nb][t][1] = kv4::pack2<false>(c23.x * f, c67.x * f);
+          qf[nb][t][2] = kv4::pack2<false>(c01.y * f, c45.y * f);
+          qf[nb][t][3] = kv4::pack2<false>(c23.y * f, c67.y * f);
+          const float2 e0 = kv4::unpack2<false>(qf[nb][t][0]), e1 = kv4::unpack2<false>(qf[nb][t][1]);
+          const float2 o0 = kv4::unpack2<false>(qf[nb][t][2]), o1 = kv4::unpack2<false>(qf[nb][t][3]);
+          sums[t / kTg] += ((e0.x + e0.y) + (e1.x + e1.y)) + ((o0.x + o0.y) + (o1.x + o1.y));
+        }
+        const float unit = inv_f * p.scale_log2;
+#pragma unroll
+        for (int i = 0; i < kNg; ++i) {
+          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 1);
+          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 2);
+          sums[i] *= 8.0f * unit;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int from = (2 * q4 + j) * 4;  // a lane of that column
+          cs[nb][j] = __shfl_sync(0xffffffffu, unit, from) * 0x1p18f;
+#pragma unroll
+          for (int i = 0; i < kNg; ++i) corr[nb][j][i] = __shfl_sync(0xffffffffu, sums[i], from);
+          const int tk = __shfl_sync(0xffffffffu, tok, from);
+          lim[nb][j] = tk < cur.w.queries ? seen0 + tk : cur.w.len;
+        }
+      }
+
+      // ---- its running state ----
+      float o[kT][2][NB][4], ps[kNg][NB][4];
+      float m[NB][2], mu[NB][2], l[NB][2];
+      float sig = 0x1p-100f, vmul = 0x1p105f;  // V's power of two, 2^5 over it
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[t][i][nb][c] = 0.f;
+#pragma unroll
+        for (int i = 0; i < kNg; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) ps[i][nb][c] = 0.f;
+        m[nb][0] = m[nb][1] = -INFINITY;
+        mu[nb][0] = mu[nb][1] = 0.f;
+        l[nb][0] = l[nb][1] = 0.f;
+      }
+
+#pragma unroll 1
+      for (int it = 0; it < n; ++it) {
+        kv4::cp_wait<kStages - 2>();
+        __syncwarp();  // this tile is here for all lanes, and the last one is read
+        issue(stage == 0 ? kStages - 1 : stage - 1);
+        const uint8_t* st = ring + stage * Tile::kBytes;
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+        const int key0 = (cur.t + it) * kAttnKeys;
+        if (key0 >= cur.keys) continue;  // nothing of this tile was fetched
+
+        // scores, log2 units
+        float s[2][NB][4];
+        uint32_t vsc[2][2][(kNg + 1) / 2];  // V's scales of rows g and g + 8
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          uint32_t k0[kT], k1[kT];
+          const uint8_t* kr = st + (16 * mb + key_g) * (D / 2) + q4 * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(kr);
+            const uint4 y = *reinterpret_cast<const uint4*>(kr + 8 * (D / 2));
+            k0[0] = x.x, k0[1] = x.y, k0[2] = x.z, k0[3] = x.w;
+            k1[0] = y.x, k1[1] = y.y, k1[2] = y.z, k1[3] = y.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(kr);
+            const uint2 y = *reinterpret_cast<const uint2*>(kr + 8 * (D / 2));
+            k0[0] = x.x, k0[1] = x.y;
+            k1[0] = y.x, k1[1] = y.y;
+          }
+          uint32_t ksc[2][(kNg + 1) / 2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int key = 16 * mb + 8 * h + key_g;
+            const uint8_t* kp = st + Tile::kOffKs + key * (2 * kNg);
+            const uint8_t* vp = st + Tile::kOffVs + key * (2 * kNg);
+            if constexpr (kNg == 4) {
+              const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
+              ksc[h][0] = x.x, ksc[h][1] = x.y;
+              vsc[mb][h][0] = y.x, vsc[mb][h][1] = y.y;
+            } else if constexpr (kNg == 2) {
+              ksc[h][0] = *reinterpret_cast<const uint32_t*>(kp);
+              vsc[mb][h][0] = *reinterpret_cast<const uint32_t*>(vp);
+            } else {
+              ksc[h][0] = *reinterpret_cast<const unsigned short*>(kp);
+              vsc[mb][h][0] = *reinterpret_cast<const unsigned short*>(vp);
+            }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.f;
+#pragma unroll
+          for (int i = 0; i < kNg; ++i) {
+            float acc[NB][4];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[nb][c] = 0.f;
+#pragma unroll
+            for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
+              const uint32_t x = k0[t], y = k1[t];
+              const uint32_t ev[4] = {kv4::nibble<0>(x), kv4::nibble<0>(y), kv4::nibble<2>(x),
+                                      kv4::nibble<2>(y)};
+              const uint32_t od[4] = {kv4::nibble<1>(x), kv4::nibble<1>(y), kv4::nibble<3>(x),
+                                      kv4::nibble<3>(y)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                dec::mma_f16(acc[nb], ev, qf[nb][t][0], qf[nb][t][1]);
+                dec::mma_f16(acc[nb], od, qf[nb][t][2], qf[nb][t][3]);
+              }
+            }
+            const float a0 = kv4::unpack1<BF16>((i & 1) ? ksc[0][i / 2] >> 16 : ksc[0][i / 2] & 0xffffu);
+            const float a1 = kv4::unpack1<BF16>((i & 1) ? ksc[1][i / 2] >> 16 : ksc[1][i / 2] & 0xffffu);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                s[mb][nb][j] = fmaf(fmaf(acc[nb][j], cs[nb][j], -corr[nb][j][i]), a0, s[mb][nb][j]);
+                s[mb][nb][2 + j] =
+                    fmaf(fmaf(acc[nb][2 + j], cs[nb][j], -corr[nb][j][i]), a1, s[mb][nb][2 + j]);
+              }
+          }
+        }
+        if (key0 + kAttnKeys > min_lim) {
+          // keys that a column does not see; rows past the cache hold whatever
+          // the ring held, so their V scales go too
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = key0 + 16 * mb + 8 * h + key_g;
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (key >= lim[nb][j]) s[mb][nb][2 * h + j] = -INFINITY;
+              if (key >= cur.keys) {
+#pragma unroll
+                for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = 0u;
+              }
+            }
+        }
+
+        // running maximum, and the power of two of V's scales
+        float mx[NB][2], vmax = 0.f;
+        bool moved = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            mx[nb][j] = fmaxf(fmaxf(s[0][nb][j], s[0][nb][2 + j]), fmaxf(s[1][nb][j], s[1][nb][2 + j]));
+            moved |= mx[nb][j] > m[nb][j] + 8.0f;
+          }
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < kNg; ++i)
+              vmax = fmaxf(vmax, kv4::unpack1<BF16>((i & 1) ? vsc[mb][h][i / 2] >> 16
+                                                            : vsc[mb][h][i / 2] & 0xffffu));
+        moved |= vmax >= 2.0f * sig;
+        if (__any_sync(0xffffffffu, moved)) {
+          vmax = kv4::max_over_rows(vmax);
+          const uint32_t ve = min(__float_as_uint(vmax) >> 23, 220u);
+          const float sig_new = fmaxf(sig, __uint_as_float(ve << 23));
+          const float keep = sig / sig_new;
+          sig = sig_new;
+          vmul = 32.0f / sig;
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float mn = fmaxf(m[nb][j], kv4::max_over_rows(mx[nb][j]));
+              const float to = mn == -INFINITY ? 0.f : mn;
+              const float al = ptx::ex2(m[nb][j] - to);  // 0 from -infinity
+              m[nb][j] = mn;
+              mu[nb][j] = to;
+              l[nb][j] *= al;
+              const float ao = al * keep;
+#pragma unroll
+              for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  o[t][i][nb][j] *= ao;
+                  o[t][i][nb][2 + j] *= ao;
+                }
+#pragma unroll
+              for (int i = 0; i < kNg; ++i) {
+                ps[i][nb][j] *= ao;
+                ps[i][nb][2 + j] *= ao;
+              }
+            }
+        }
+
+        // P and P V
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[mb][nb][c] = ptx::ex2(s[mb][nb][c] - mu[nb][c & 1]);
+            l[nb][0] += s[mb][nb][0] + s[mb][nb][2];
+            l[nb][1] += s[mb][nb][1] + s[mb][nb][3];
+          }
+          uint32_t v[4][kT / 2];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = 16 * mb + 8 * (e >> 1) + ((e & 1) ? key_e1 : key_e0);
+            const uint8_t* vr = st + Tile::kOffV + key * (D / 2) + v_sw;
+            if constexpr (D == 128) {
+              const uint2 x = *reinterpret_cast<const uint2*>(vr);
+              v[e][0] = x.x, v[e][1] = x.y;
+            } else {
+              v[e][0] = *reinterpret_cast<const uint32_t*>(vr);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kNg; ++i) {
+            const float f0 =
+                vmul * kv4::unpack1<BF16>((i & 1) ? vsc[mb][0][i / 2] >> 16 : vsc[mb][0][i / 2] & 0xffffu);
+            const float f1 =
+                vmul * kv4::unpack1<BF16>((i & 1) ? vsc[mb][1][i / 2] >> 16 : vsc[mb][1][i / 2] & 0xffffu);
+            uint32_t pb[NB][2];
+            const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              pb[nb][0] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][0] * f0, s[mb][nb][1] * f0));
+              pb[nb][1] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][2] * f1, s[mb][nb][3] * f1));
+              dec::mma_f16(ps[i][nb], ones, pb[nb][0], pb[nb][1]);
+            }
+#pragma unroll
+            for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
+              // channels 32 t + 4 g + {0, 2} and {1, 3} of keys e0, e1 | e2, e3
+              const uint32_t pick = (t & 1) ? 0x7632u : 0x5410u;
+              const uint32_t x = __byte_perm(v[0][t / 2], v[1][t / 2], pick);
+              const uint32_t y = __byte_perm(v[2][t / 2], v[3][t / 2], pick);
+              const uint32_t ev[4] = {kv4::nibble<0>(x), kv4::nibble<2>(x), kv4::nibble<0>(y),
+                                      kv4::nibble<2>(y)};
+              const uint32_t od[4] = {kv4::nibble<1>(x), kv4::nibble<3>(x), kv4::nibble<1>(y),
+                                      kv4::nibble<3>(y)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                dec::mma_f16(o[t][0][nb], ev, pb[nb][0], pb[nb][1]);
+                dec::mma_f16(o[t][1][nb], od, pb[nb][0], pb[nb][1]);
+              }
+            }
+          }
+        }
+      }
+
+      // ---- the unit's end: to the outputs, or a partial state ----
+      float* part = nullptr;
+      if (!whole) {
+        // a warp's last tiles leave their state in its ring, which is done with;
+        // an earlier unit's (one at most: the warp's first) goes to the workspace
+        if (head)
+          part = p.heads + static_cast<size_t>(blockIdx.x * kAttnWarps + warp) * kv4::kPartFloats<D, NB>;
+        else {
+          kv4::cp_wait<0>();
+          __syncwarp();
+          part = reinterpret_cast<float*>(ring);
+        }
+      }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float lsum = kv4::sum_over_rows(l[nb][j]);
+          const int col = 8 * nb + 2 * q4 + j;
+          int tok, row, hq;
+          const bool on = kv4::column<NB>(p, cur.w, cur.kv, cur.block, col, &tok, &row, &hq);
+          const float down = whole ? (lsum == 0.f ? 0.f : 0.03125f * sig / lsum) : 0.03125f * sig;
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
+            const float off = 8.0f * ps[t / kTg][nb][j];
+            float4 x;
+            x.x = fmaf(o[t][0][nb][j], 0x1p18f, -off) * down;
+            x.y = fmaf(o[t][1][nb][j], 0x1p18f, -off) * down;
+            x.z = fmaf(o[t][0][nb][2 + j], 0x1p18f, -off) * down;
+            x.w = fmaf(o[t][1][nb][2 + j], 0x1p18f, -off) * down;
+            const int ch = 32 * t + 4 * g;
+            if (!whole)
+              *reinterpret_cast<float4*>(part + col * D + ch) = x;
+            else if (on)
+              *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
+                  make_uint2(kv4::pack2<BF16>(x.x, x.y), kv4::pack2<BF16>(x.z, x.w));
+          }
+          if (g == 0) {
+            if (!whole) {
+              part[kCols * D + col] = m[nb][j];
+              part[kCols * (D + 1) + col] = lsum;
+            } else if (on && p.lse) {
+              p.lse[static_cast<size_t>(hq) * p.total_q + row] =
+                  lsum == 0.f ? -INFINITY : (m[nb][j] + __log2f(lsum)) * 0.69314718055994530942f;
+            }
+          }
+        }
+      if (!whole && lane == 0)
+        parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur.s, cur.kv, cur.block, cur.w.tiles, part};
+      left -= n;
+      unit_first += cur.w.tiles;
+      if (left > 0 && !cur.next_unit(p)) break;
+    }
+    kv4::cp_wait<0>();
+  }
+
+  // ---- the CTA's partial states, unit by unit; what other CTAs share goes on ----
+  __syncthreads();
+  float* weight = reinterpret_cast<float*>(attn_smem + kAttnWarps * kStages * Tile::kBytes);
+  // Combines the states that `at(i)`, i < n, points to: to the unit's outputs,
+  // or (out) to another state.
+  const auto combine = [&](const kv4::Part& u, int n, auto at, auto load, float* out) {
+    // weights 2^(m_i - M) of each column; [n][kCols]
+    for (int x = tid; x < n * kCols; x += kAttnThreads)
+      weight[x] = load(at(x / kCols) + kCols * D + x % kCols);
+    __syncthreads();
+    for (int col = warp; col < kCols; col += kAttnWarps) {
+      float mm = -INFINITY;
+      for (int i = lane; i < n; i += 32) mm = fmaxf(mm, weight[i * kCols + col]);
+#pragma unroll
+      for (int by = 16; by > 0; by >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, by));
+      const float to = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      for (int i = lane; i < n; i += 32) {
+        const float w = ptx::ex2(weight[i * kCols + col] - to);
+        weight[i * kCols + col] = w;
+        ll += w * load(at(i) + kCols * (D + 1) + col);
+      }
+#pragma unroll
+      for (int by = 16; by > 0; by >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, by);
+      if (lane == 0) {
+        top[col] = mm;
+        sum[col] = ll;
+      }
+    }
+    __syncthreads();
+    for (int x = tid; x < kCols * (D / 4); x += kAttnThreads) {
+      const int col = x / (D / 4), ch = 4 * (x % (D / 4));
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float w = weight[i * kCols + col];
+        const float4 y = load(reinterpret_cast<const float4*>(at(i) + col * D + ch));
+        acc.x = fmaf(w, y.x, acc.x);
+        acc.y = fmaf(w, y.y, acc.y);
+        acc.z = fmaf(w, y.z, acc.z);
+        acc.w = fmaf(w, y.w, acc.w);
+      }
+      const float mm = top[col], ll = sum[col];
+      if (out) {
+        *reinterpret_cast<float4*>(out + col * D + ch) = acc;
+        if (ch == 0) {
+          out[kCols * D + col] = mm;
+          out[kCols * (D + 1) + col] = ll;
+        }
+      } else {
+        const kv4::SeqWork sw = kv4::seq_work<NB>(p, u.s);
+        int tok, row, hq;
+        if (kv4::column<NB>(p, sw, u.kv, u.block, col, &tok, &row, &hq)) {
+          const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+          *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
+              make_uint2(kv4::pack2<BF16>(acc.x * inv, acc.y * inv),
+                         kv4::pack2<BF16>(acc.z * inv, acc.w * inv));
+          if (ch == 0 && p.lse)
+            p.lse[static_cast<size_t>(hq) * p.total_q + row] =
+                ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * 0.69314718055994530942f;
+        }
+      }
+    }
+    __syncthreads();
+  };
+  for (int e = 0; e < 2 * kAttnWarps;) {
+    if (!parts[e].at) {
+      ++e;
+      continue;
+    }
+    // the run of states of one unit (the absent ones between them are skipped)
+    const kv4::Part u = parts[e];
+    int n = 0, f = e;
+    for (; f < 2 * kAttnWarps; ++f) {
+      if (!parts[f].at) continue;
+      if (parts[f].first != u.first) break;
+      if (tid == 0) run[n] = parts[f].at;
+      ++n;
+    }
+    e = f;
+    __syncthreads();
+    const auto of_run = [&](int i) { return static_cast<const float*>(run[i]); };
+    const auto plain = [](const auto* x) { return *x; };  // shared memory, or this CTA's own
+    if (u.first >= a && u.first + u.tiles <= b) {
+      combine(u, n, of_run, plain, nullptr);
+      continue;
+    }
+    // The unit is shared with other CTAs: this one's state goes to its first
+    // place (the unit began before this CTA's tiles) or its second, and the
+    // last of the unit's CTAs to arrive combines them all, in order.
+    constexpr int kPart = kv4::kPartFloats<D, NB>;
+    combine(u, n, of_run, plain,
+            p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart);
+    const auto cta_of = [&](long long x) {  // the CTA whose tiles hold tile x
+      return static_cast<int>(((x + 1) * ctas - 1) / total);
+    };
+    const int c0 = cta_of(u.first), c1 = cta_of(u.first + u.tiles - 1);
+    if (tid == 0) {
+      __threadfence();
+      // wraps to zero with the last arrival, so the array is zero again
+      merge_last = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+      __threadfence();
+    }
+    __syncthreads();
+    if (merge_last)
+      combine(u, c1 - c0 + 1,
+              [&](int i) {
+                return static_cast<const float*>(
+                    p.parts + (2 * static_cast<size_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPart);
+              },
+              [](const auto* x) { return __ldcg(x); }, nullptr);
+    __syncthreads();
+  }
+}
+
+constexpr int kAttnMaxCtas = 1024;  // TILEMIX_KV4_SYNC_WORDS
+
+Kv4AttnShape kv4_attn_shape(const Kv4Format&, int sms, long long columns) {
+  return {sms < kAttnMaxCtas ? sms : kAttnMaxCtas, kAttnWarps, columns > 8 ? 16 : 8};
+}
+
+struct LaunchAttn {
+  const Kv4AttnParams& p;
+  const Kv4AttnShape& shape;
+  cudaStream_t stream;
+  template <int D, int GROUP, bool BF16>
+  int operator()() const {
+    return shape.cols == 8 ? run<D, GROUP, 1, BF16>() : run<D, GROUP, 2, BF16>();
+  }
+  template <int D, int GROUP, int NB, bool BF16>
+  int run() const {
+    using Tile = AttnTile<D, GROUP>;
+    const int slots = shape.ctas > 2 * kAttnWarps ? shape.ctas : 2 * kAttnWarps;
+    const int smem = kAttnWarps * Tile::kStages * Tile::kBytes + slots * 8 * NB * 4;
+    const auto kernel = kv4_attn_kernel<D, GROUP, NB, BF16>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    kernel<<<shape.ctas, kAttnThreads, smem, stream>>>(p);
+    return static_cast<int>(cudaGetLastError());
+  }
+};
+int launch_kv4_attn(const Kv4AttnParams& p, const Kv4Format& f, const Kv4AttnShape& shape,
+                    cudaStream_t stream) {
+  return for_kv4_format(f, LaunchAttn{p, shape, stream});
+}
+
+}  // namespace tilemix

@@ -1,0 +1,277 @@
+// Rows into and out of the paged 4-bit cache (tilemix_kv4_append,
+// tilemix_kv4_gather).
+//
+// Both are one pass over memory, a thread to each chunk of 8 channels: 16
+// bytes of activations against one 4-byte word of codes.  A group of channels
+// is 4, 8 or 16 neighbouring lanes, which take its largest magnitude with
+// shuffles; nothing is staged.
+//
+// Rounding.  s = a / 7 is never within 2^-15 (relative) of a midpoint of the
+// scale's type, as 7 divides no midpoint of an 11-bit significand, so one fp32
+// multiply by 1/7 and one conversion give the correctly rounded s.  The
+// quotient x / s of two significands of at most 11 bits is a half-integer or
+// at least 1 / 4094 away from every half-integer below 7.  The reciprocal
+// product is within 2^-19 of the quotient, so rounding it to a multiple of
+// 2^-12 moves no quotient across a half-integer and puts every tie exactly
+// on one, and the second rounding (to an integer, ties to even) gives
+// rne(x / s) as IEEE division would.
+// Included by tilemix_kv4.cu.
+#pragma once
+
+namespace tilemix {
+
+constexpr int kRowThreads = 256;
+
+namespace kv4 {
+
+// Two packed values of the activations' type to fp32.
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t u) {
+  if constexpr (BF16)
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+  else
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ float unpack1(uint32_t bits) {
+  if constexpr (BF16)
+    return __uint_as_float(bits << 16);
+  else
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack1(float x) {
+  if constexpr (BF16)
+    return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+  else
+    return __half_as_ushort(__float2half_rn(x));
+}
+// Bit pattern of the type's infinity: magnitudes from it on are not finite.
+template <bool BF16>
+constexpr uint32_t kInfBits = BF16 ? 0x7f80u : 0x7c00u;
+
+// Largest magnitude of a chunk, as a bit pattern (magnitudes of a type are
+// ordered like their patterns, NaNs above all).
+__device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = __vmaxu2(__vmaxu2(u.x & m, u.y & m), __vmaxu2(u.z & m, u.w & m));
+  return max(a & 0xffffu, a >> 16);
+}
+
+// The eight codes + 8 of a chunk as nibbles, channel 0 lowest.  r = 4096 / s
+// (0 for s = 0), up = 1 or the power of two that r's s was multiplied by.
+constexpr float kShift = 12582912.0f;  // 1.5 * 2^23: x + kShift is rne(x) + kShift
+template <bool BF16>
+__device__ __forceinline__ uint32_t code_word(const uint4& u, float r, float up) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack2<BF16>(w[i]);
+    c[2 * i] = x.x * up;
+    c[2 * i + 1] = x.y * up;
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // 4096 x / s, rounded to an integer; beyond +-7 only where s is subnormal
+    const float t = fminf(fmaxf(fmaf(c[i], r, kShift) - kShift, -28672.0f), 28672.0f);
+    // its 2^-12th, rounded to an integer, + 8, in the low bits of the sum
+    const uint32_t b = __float_as_uint(fmaf(t, 0x1p-12f, kShift + 8.0f));
+    word |= (b & 15u) << (4 * i);
+  }
+  return word;
+}
+
+// Place of a row's 32-bit word of K holding channels 8w .. 8w + 7.
+template <int D>
+__device__ __forceinline__ int k_place(int w) {
+  return (w & 3) * (D / 32) + (w >> 2);
+}
+
+}  // namespace kv4
+
+// One chunk of 8 channels per thread; blockIdx.y picks K or V.
+template <int D, int GROUP, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendParams p) {
+  constexpr int kChunks = D / 8;  // of a row: 8 or 16, so a warp holds whole rows
+  constexpr int T = D / 32;
+  const bool is_v = blockIdx.y != 0;
+  const uint32_t per_token = p.pool.hk * kChunks;
+  const uint32_t chunks = static_cast<uint32_t>(p.n) * per_token;
+  const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
+  const bool live = i < chunks;
+  const uint32_t token = live ? i / per_token : 0u;
+  const uint32_t in_token = live ? i - token * per_token : 0u;
+  const int slot = live ? __ldg(p.slots + token) : -1;
+  const bool ok = slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
+  uint4 u = make_uint4(0u, 0u, 0u, 0u);
+  if (ok)
+    u = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v + token * p.v_stride
+                                                   : p.k + token * p.k_stride) +
+                                             in_token * 16));
+  uint32_t a = kv4::absmax_bits(u);
+#pragma unroll
+  for (int by = GROUP / 16; by > 0; by >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, by));
+  const bool finite = a < kv4::kInfBits<BF16>;
+  const uint32_t sbits =
+      finite ? kv4::pack1<BF16>(kv4::unpack1<BF16>(a) * (1.0f / 7.0f)) : kv4::kInfBits<BF16> + 1u;
+  // 4096 / s; a bfloat16 s below 2^-100 is lifted first, so that it stays finite
+  const float s = finite ? kv4::unpack1<BF16>(sbits) : 0.f;
+  const float up = BF16 && s < 0x1p-100f ? 0x1p64f : 1.0f;
+  const float r = s > 0.f ? __frcp_rn(s * up) * 4096.0f : 0.f;
+  uint32_t word = finite ? kv4::code_word<BF16>(u, r, up) : 0x88888888u;
+  const int head = in_token / kChunks, w = in_token % kChunks;
+  const size_t row = ((static_cast<size_t>(slot >> p.pool.page_shift) * p.pool.hk + head)
+                      << p.pool.page_shift) +
+                     (slot & ((1 << p.pool.page_shift) - 1));
+  int place;
+  if (!is_v) {
+    place = kv4::k_place<D>(w);
+  } else {
+    // V's halfwords 2w and 2w + 1 lie apart: halfword 8t + g at place g T + t.
+    // The lane four on holds the same places of the next t: each of the two
+    // lanes sends one half and keeps a whole 32-bit word.
+    const int t = w >> 2;
+    const uint32_t other =
+        __shfl_xor_sync(0xffffffffu, (t & 1) ? word & 0xffffu : word >> 16, 4);
+    const int g = 2 * (w & 3) + (t & 1);
+    word = (t & 1) ? __byte_perm(other, word, 0x7610) : __byte_perm(word, other, 0x5410);
+    place = g * (T / 2) + (t >> 1);
+  }
+  if (ok) {
+    uint8_t* codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + row * (D / 2);
+    *reinterpret_cast<uint32_t*>(codes + place * 4) = word;
+    if (w % (GROUP / 8) == 0) {
+      uint8_t* scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + row * (2 * (D / GROUP));
+      *reinterpret_cast<unsigned short*>(scales + 2 * (w / (GROUP / 8))) =
+          static_cast<unsigned short>(sbits);
+    }
+  } else if (live && slot != -1) {
+    atomicOr(&g_kv4_status, kStatusBadPages);
+  }
+}
+
+// blockIdx.y: sequence; blockIdx.z: K or V; the CTAs of blockIdx.x
+// stride over the sequence's chunks.
+template <int D, int GROUP, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherParams p) {
+  constexpr int kChunks = D / 8;
+  constexpr int T = D / 32;
+  const bool is_v = blockIdx.z != 0;
+  const int s = blockIdx.y, sh = p.pool.page_shift;
+  const long long top = static_cast<long long>(p.max_pages) << sh;
+  const int have = __ldg(p.seq_len + s);
+  const int len = static_cast<int>(min(static_cast<long long>(max(have, 0)), top));
+  bool bad = have != len;
+  const long long out0 = __ldg(p.out_start + s);
+  const uint32_t per_token = p.pool.hk * kChunks;
+  const uint8_t* codes = is_v ? p.pool.v_codes : p.pool.k_codes;
+  const uint8_t* scales = is_v ? p.pool.v_scale : p.pool.k_scale;
+  uint8_t* out = is_v ? p.v : p.k;
+  const int32_t* table = p.block_table + static_cast<size_t>(s) * p.max_pages;
+  // token and chunk of the token, carried along without a division per step
+  const uint32_t first = blockIdx.x * kRowThreads + threadIdx.x;
+  const uint32_t step = gridDim.x * kRowThreads;  // < 2^25
+  const uint32_t step_pos = step / per_token, step_in = step % per_token;
+  uint32_t in_next = first % per_token;
+  long long pos_next = first / per_token;
+  while (pos_next < len) {
+    const uint32_t pos = static_cast<uint32_t>(pos_next), in_token = in_next;
+    pos_next += step_pos;
+    in_next += step_in;
+    if (in_next >= per_token) {
+      in_next -= per_token;
+      ++pos_next;
+    }
+    const int page = __ldg(table + (pos >> sh));
+    const long long to = out0 + pos;
+    if (page < 0 || page >= p.pool.num_pages || to < 0 || to >= p.rows) {
+      bad = true;
+      continue;
+    }
+    const int head = in_token / kChunks, w = in_token % kChunks;
+    const size_t row =
+        ((static_cast<size_t>(page) * p.pool.hk + head) << sh) + (pos & ((1u << sh) - 1));
+    uint32_t word;
+    if (!is_v) {
+      word = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + kv4::k_place<D>(w));
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(codes + row * (D / 2)) +
+                                2 * (w & 3) * T + (w >> 2);
+      word = __ldg(h) | (static_cast<uint32_t>(__ldg(h + T)) << 16);
+    }
+    const float sc = kv4::unpack1<BF16>(__ldg(
+        reinterpret_cast<const unsigned short*>(scales + row * (2 * (D / GROUP))) + w / (GROUP / 8)));
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float lo = static_cast<float>(static_cast<int>((word >> (8 * k)) & 15u) - 8);
+      const float hi = static_cast<float>(static_cast<int>((word >> (8 * k + 4)) & 15u) - 8);
+      o[k] = kv4::pack2<BF16>(lo * sc, hi * sc);
+    }
+    *reinterpret_cast<uint4*>(out + (static_cast<size_t>(to) * per_token + in_token) * 16) =
+        make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  if (bad) atomicOr(&g_kv4_status, kStatusBadPages);
+}
+
+// Calls fn.template operator()<D, GROUP, BF16>() for the format.
+template <class Fn>
+int for_kv4_format(const Kv4Format& f, Fn fn) {
+  if (f.d == 128) {
+    if (f.group == 32) return f.bf16 ? fn.template operator()<128, 32, true>() : fn.template operator()<128, 32, false>();
+    if (f.group == 64) return f.bf16 ? fn.template operator()<128, 64, true>() : fn.template operator()<128, 64, false>();
+    if (f.group == 128) return f.bf16 ? fn.template operator()<128, 128, true>() : fn.template operator()<128, 128, false>();
+  } else if (f.d == 64) {
+    if (f.group == 32) return f.bf16 ? fn.template operator()<64, 32, true>() : fn.template operator()<64, 32, false>();
+    if (f.group == 64) return f.bf16 ? fn.template operator()<64, 64, true>() : fn.template operator()<64, 64, false>();
+  }
+  return cudaErrorInvalidValue;
+}
+
+struct LaunchAppend {
+  const Kv4AppendParams& p;
+  cudaStream_t stream;
+  template <int D, int GROUP, bool BF16>
+  int operator()() const {
+    const long long chunks = static_cast<long long>(p.n) * p.pool.hk * (D / 8);
+    const dim3 grid(static_cast<unsigned>((chunks + kRowThreads - 1) / kRowThreads), 2);
+    kv4_append_kernel<D, GROUP, BF16><<<grid, kRowThreads, 0, stream>>>(p);
+    return static_cast<int>(cudaGetLastError());
+  }
+};
+int launch_kv4_append(const Kv4AppendParams& p, const Kv4Format& f, cudaStream_t stream) {
+  return for_kv4_format(f, LaunchAppend{p, stream});
+}
+
+struct LaunchGather {
+  const Kv4GatherParams& p;
+  cudaStream_t stream;
+  template <int D, int GROUP, bool BF16>
+  int operator()() const {
+    // about 32 resident CTAs' worth per SM over all sequences
+    const long long most = static_cast<long long>(p.rows) * p.pool.hk * (D / 8);
+    long long per_seq = (most / p.nseq + kRowThreads - 1) / kRowThreads;
+    if (per_seq < 1) per_seq = 1;
+    if (per_seq > 65535) per_seq = 65535;
+    const dim3 grid(static_cast<unsigned>(per_seq), p.nseq, 2);
+    kv4_gather_kernel<D, GROUP, BF16><<<grid, kRowThreads, 0, stream>>>(p);
+    return static_cast<int>(cudaGetLastError());
+  }
+};
+int launch_kv4_gather(const Kv4GatherParams& p, const Kv4Format& f, cudaStream_t stream) {
+  return for_kv4_format(f, LaunchGather{p, stream});
+}
+
+}  // namespace tilemix

@@ -1,0 +1,278 @@
+"""Paged 4-bit K/V cache: the call site of ``tilemix_page_plan``,
+``tilemix_kv4_append``, ``tilemix_kv4_gather`` and ``tilemix_kv4_attn``.
+
+One object holds a pool of pages, the batch's block table, lengths and free
+stack (all on the device), and the attention's workspaces.  A step is
+
+    plan = cache.plan(new_len, max_tokens=n)      # pages and slots
+    cache.append(k, v, plan.slots)                # rows in, 4 bits
+    o = cache.attend(q, max_seqlen, token_start=plan.token_start, max_new=m)
+
+and none of it reads anything back to the host.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from . import (KV_DTYPES, KV4_SYNC_WORDS, KV4AppendArgs, KV4AttnArgs, KV4Cache, KV4GatherArgs,
+               PagePlanArgs, lib, tilemix_kv4_append, tilemix_kv4_attn,
+               tilemix_kv4_attn_workspace_size, tilemix_kv4_gather, tilemix_page_plan)
+
+
+class PagePlan(NamedTuple):
+    """Outputs of a plan, int32 on the device: token_start [nseq + 1] (the first
+    of each sequence's new tokens), slots [max_tokens], granted [nseq]."""
+    token_start: torch.Tensor
+    slots: torch.Tensor
+    granted: torch.Tensor
+
+
+def _dtype_id(dtype):
+    names = {torch.float16: "fp16", torch.bfloat16: "bf16"}
+    if dtype not in names:
+        raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+    return KV_DTYPES[names[dtype]]
+
+
+class TileMixKV4Cache:
+    """max_seqs sequences with up to max_pages pages each, over num_pages pages
+    of page_size tokens; hk KV heads of d channels, one scale per `group`
+    channels.  Sequences are rows 0 .. max_seqs - 1 of the tables and start
+    empty; the calls take the first nseq of them.
+
+    pool     (k_codes, k_scale, v_codes, v_scale) to use instead of new ones
+    tables   (block_table [max_seqs, max_pages], seq_len [max_seqs],
+             free_list [num_pages], free_count [1]), int32, likewise
+
+    The object belongs to one device, whichever is current; `stream` picks the
+    stream of a call (default: the current one of that device).  Two calls that
+    change the same tables or rows, or read what another writes, must be ordered
+    by the caller, as for any tensor.  attend() keeps a workspace per stream, so
+    calls on different streams may run at the same time; a call that is being
+    captured into a CUDA graph takes one from the graph's own memory."""
+
+    def __init__(self, num_pages, page_size, hk, d, max_seqs, max_pages, group=32,
+                 dtype=torch.float16, device="cuda", pool=None, tables=None):
+        lib()
+        self.num_pages, self.page_size = int(num_pages), int(page_size)
+        self.hk, self.d, self.group = int(hk), int(d), int(group)
+        self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
+        self.dtype = dtype
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("the cache lives on a CUDA device")
+        if self.d not in (64, 128) or self.group not in (32, 64, 128) or self.group > self.d:
+            raise ValueError("d is 64 or 128, group 32, 64 or 128 and at most d")
+        if min(self.num_pages, self.page_size, self.hk, self.max_seqs, self.max_pages) < 1:
+            raise ValueError("sizes start at 1")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        dev, i32 = self.device, torch.int32
+        rows = (self.num_pages, self.hk, self.page_size)
+        shapes = [(rows + (self.d // 2,), torch.uint8), (rows + (self.d // self.group,), dtype)] * 2
+        dt = _dtype_id(dtype)
+        if pool is None:
+            pool = [torch.zeros(s, dtype=t, device=dev) for s, t in shapes]
+        for x, (s, t) in zip(pool, shapes, strict=True):
+            self._expect(x, t, s, "pool")
+        shapes = [((self.max_seqs, self.max_pages), i32), ((self.max_seqs,), i32),
+                  ((self.num_pages,), i32), ((1,), i32)]
+        if tables is None:
+            tables = (torch.full(shapes[0][0], -1, dtype=i32, device=dev),
+                      torch.zeros(self.max_seqs, dtype=i32, device=dev),
+                      torch.arange(self.num_pages - 1, -1, -1, dtype=i32, device=dev),
+                      torch.full((1,), self.num_pages, dtype=i32, device=dev))
+        for x, (s, t) in zip(tables, shapes, strict=True):
+            self._expect(x, t, s, "tables")
+        self.k_codes, self.k_scale, self.v_codes, self.v_scale = pool
+        self.block_table, self.seq_len, self.free_list, self.free_count = tables
+        c = KV4Cache()
+        c.k_codes, c.k_scale = self.k_codes.data_ptr(), self.k_scale.data_ptr()
+        c.v_codes, c.v_scale = self.v_codes.data_ptr(), self.v_scale.data_ptr()
+        c.num_pages, c.page_size, c.hk, c.d = self.num_pages, self.page_size, self.hk, self.d
+        c.group, c.dtype = self.group, dt
+        self._plan = PagePlanArgs()
+        self._plan.seq_len, self._plan.block_table = self.seq_len.data_ptr(), self.block_table.data_ptr()
+        self._plan.free_list, self._plan.free_count = self.free_list.data_ptr(), self.free_count.data_ptr()
+        self._plan.max_pages, self._plan.num_pages = self.max_pages, self.num_pages
+        self._plan.page_size = self.page_size
+        self._append = KV4AppendArgs(cache=c)
+        self._gather = KV4GatherArgs(cache=c, max_pages=self.max_pages)
+        self._gather.block_table, self._gather.seq_len = self.block_table.data_ptr(), self.seq_len.data_ptr()
+        self._attn = KV4AttnArgs(cache=c, max_pages=self.max_pages)
+        self._attn.block_table, self._attn.seq_len = self.block_table.data_ptr(), self.seq_len.data_ptr()
+        self._spaces = {}
+
+    # ---------------------------------------------------------------- checks
+
+    def _expect(self, x, dtype, shape, what):
+        """x is a contiguous tensor of this device; a None in shape matches any size."""
+        if x.dtype != dtype or x.device != self.device or not x.is_contiguous() or \
+                x.dim() != len(shape) or any(n is not None and a != n for a, n in zip(x.shape, shape)):
+            raise ValueError("%s: expected a contiguous %s tensor of shape %s on %s, got %s %s on %s"
+                             % (what, dtype, tuple(shape), self.device, x.dtype, tuple(x.shape), x.device))
+
+    def _nseq(self, x, what, extra=0):
+        n = x.shape[0] - extra
+        if not 0 <= n <= self.max_seqs:
+            raise ValueError("%s: the cache holds %d sequences" % (what, self.max_seqs))
+        return n
+
+    def _on(self, stream, fn, *args):
+        """fn(*args) with this object's device, and `stream`, current."""
+        if stream is not None:
+            if stream.device != self.device:
+                raise ValueError("the stream belongs to %s, the cache to %s" % (stream.device, self.device))
+            with torch.cuda.stream(stream):
+                return fn(*args)
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return fn(*args)
+        return fn(*args)
+
+    # ----------------------------------------------------------------- calls
+
+    def new_plan(self, max_tokens, nseq=None):
+        """Buffers of a plan, for plan(out=...)."""
+        n = self.max_seqs if nseq is None else int(nseq)
+        new = lambda m: torch.empty(m, dtype=torch.int32, device=self.device)
+        return PagePlan(new(n + 1), new(int(max_tokens)), new(n))
+
+    def plan(self, new_len, max_tokens=None, out=None, stream=None):
+        """Pages and slots for new_len[s] more tokens (fewer, if negative) of each
+        sequence (see tilemix_page_plan).  new_len: int32 [nseq] on the device;
+        max_tokens: the number of slots, or `out` from new_plan()."""
+        return self._on(stream, self._plan_call, new_len, max_tokens, out)
+
+    def _plan_call(self, new_len, max_tokens, out):
+        n = self._nseq(new_len, "new_len")
+        self._expect(new_len, torch.int32, (n,), "new_len")
+        if out is None:
+            if max_tokens is None:
+                raise ValueError("max_tokens or out")
+            out = self.new_plan(max_tokens, n)
+        else:
+            if max_tokens is not None and max_tokens != out.slots.shape[0]:
+                raise ValueError("max_tokens is %d, out has %d slots" % (max_tokens, out.slots.shape[0]))
+            self._expect(out.token_start, torch.int32, (n + 1,), "token_start")
+            self._expect(out.slots, torch.int32, (None,), "slots")
+            self._expect(out.granted, torch.int32, (n,), "granted")
+        a = self._plan
+        a.new_len, a.nseq = new_len.data_ptr(), n
+        a.token_start, a.granted = out.token_start.data_ptr(), out.granted.data_ptr()
+        a.slots, a.max_tokens = out.slots.data_ptr(), out.slots.shape[0]
+        if n == 0:  # an empty tensor has no address
+            a.new_len = a.granted = out.token_start.data_ptr()
+        tilemix_page_plan(a)
+        return out
+
+    def append(self, k, v, slots, stream=None):
+        """Rows of k and v [n, hk, d] (the heads of a token contiguous, tokens at
+        any stride) to slots [n] (int32; -1: skipped)."""
+        return self._on(stream, self._append_call, k, v, slots)
+
+    def _append_call(self, k, v, slots):
+        n = slots.shape[0]
+        self._expect(slots, torch.int32, (n,), "slots")
+        a = self._append
+        for x, what in ((k, "k"), (v, "v")):
+            if x.dtype != self.dtype or x.device != self.device or x.dim() != 3 or \
+                    x.shape[0] < n or x.shape[1] != self.hk or x.shape[2] != self.d:
+                raise ValueError("%s: expected %s [%d or more, %d, %d] on %s" %
+                                 (what, self.dtype, n, self.hk, self.d, self.device))
+            if x.stride(2) != 1 or (self.hk > 1 and x.stride(1) != self.d):
+                raise ValueError("%s: a token's heads must be contiguous" % what)
+        if n == 0:
+            return
+        row = self.hk * self.d
+        a.k, a.v, a.slots, a.n = k.data_ptr(), v.data_ptr(), slots.data_ptr(), n
+        a.k_stride = k.stride(0) if k.shape[0] > 1 else row
+        a.v_stride = v.stride(0) if v.shape[0] > 1 else row
+        tilemix_kv4_append(a)
+
+    def gather(self, out_start, rows, out=None, stream=None):
+        """K and V of the sequences' tokens as 16-bit values: position p of
+        sequence s at row out_start[s] + p (int32 [nseq]) of two [rows, hk, d]
+        tensors (`out`, or new ones)."""
+        return self._on(stream, self._gather_call, out_start, rows, out)
+
+    def _gather_call(self, out_start, rows, out):
+        n = self._nseq(out_start, "out_start")
+        self._expect(out_start, torch.int32, (n,), "out_start")
+        rows = int(rows)
+        shape = (rows, self.hk, self.d)
+        if out is None:
+            out = (torch.empty(shape, dtype=self.dtype, device=self.device),
+                   torch.empty(shape, dtype=self.dtype, device=self.device))
+        else:
+            for x in out:
+                self._expect(x, self.dtype, shape, "out")
+        a = self._gather
+        a.out_start, a.nseq, a.rows = out_start.data_ptr(), n, rows
+        a.k, a.v = out[0].data_ptr(), out[1].data_ptr()
+        tilemix_kv4_gather(a)
+        return tuple(out)
+
+    def attend(self, q, max_seqlen, token_start=None, max_new=1, softmax_scale=0.0, out=None,
+               lse=False, stream=None):
+        """Attention of the newest tokens over the cache (see tilemix_kv4_attn).
+        q [rows, hq, d]: sequence s's queries are rows token_start[s] ..
+        token_start[s + 1] - 1 (int32 [nseq + 1]), or row s if token_start is
+        None.  max_seqlen and max_new bound the lengths and the queries per
+        sequence.  Returns o like q, or (o, LSE [hq, rows]) if lse; `out` and a
+        tensor as `lse` are written in place.  Rows that no sequence covers are
+        not written (in a new tensor they hold nothing meaningful)."""
+        return self._on(stream, self._attend_call, q, max_seqlen, token_start, max_new,
+                        softmax_scale, out, lse)
+
+    def _attend_call(self, q, max_seqlen, token_start, max_new, softmax_scale, out, lse):
+        self._expect(q, self.dtype, (None, None, self.d), "q")
+        rows, hq = q.shape[0], q.shape[1]
+        if hq < 1 or hq % self.hk != 0:
+            raise ValueError("q has %d heads, the cache %d" % (hq, self.hk))
+        a = self._attn
+        if token_start is None:
+            n = self._nseq(q, "q")
+            a.token_start = None
+        else:
+            n = self._nseq(token_start, "token_start", 1)
+            self._expect(token_start, torch.int32, (n + 1,), "token_start")
+            a.token_start = token_start.data_ptr()
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._expect(out, self.dtype, q.shape, "out")
+        want = lse is not None and lse is not False
+        if lse is True:
+            lse = torch.empty((hq, rows), dtype=torch.float32, device=self.device)
+        elif want:
+            self._expect(lse, torch.float32, (hq, rows), "lse")
+        a.q, a.o = q.data_ptr(), out.data_ptr()
+        a.lse = lse.data_ptr() if want else None
+        a.nseq, a.total_q, a.hq = n, rows, hq
+        a.max_new, a.max_seqlen, a.softmax_scale = int(max_new), int(max_seqlen), float(softmax_scale)
+        if rows and n:
+            space = self._space(a)
+            a.workspace, a.workspace_bytes = space[0].data_ptr(), space[0].shape[0]
+            a.sync = space[1].data_ptr()
+        tilemix_kv4_attn(a)
+        return (out, lse) if want else out
+
+    def _space(self, a):
+        """(workspace, sync words) of the current stream."""
+        key = torch.cuda.current_stream().cuda_stream
+        if torch.cuda.is_current_stream_capturing():
+            # a graph's own: its replays must not share one with calls outside it
+            nbytes = tilemix_kv4_attn_workspace_size(a)
+            return (torch.empty(nbytes, dtype=torch.uint8, device=self.device),
+                    torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device))
+        cols = a.max_new * a.hq > 8 * self.hk
+        space = self._spaces.get((key, cols))
+        if space is None:
+            nbytes = tilemix_kv4_attn_workspace_size(a)
+            space = (torch.empty(nbytes, dtype=torch.uint8, device=self.device),
+                     torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device))
+            self._spaces[(key, cols)] = space
+        return space

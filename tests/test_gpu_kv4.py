@@ -307,8 +307,8 @@ def _attend(pool, queries, hq, seed=0, q_scale=1.0, scale=0.0, max_new=None, cac
     o, l = kc.to_numpy(out), kc.to_numpy(lse)
     assert (o[n:] == 7.0).all() and (l[:, n:] == 7.0).all()  # rows behind the last sequence
     worst = kc.check_attend(o, l, q, pool, pool.lengths, start, hq, scale or None)
-    for _, sync in cache._spaces.values():
-        assert not sync.any()
+    for space in cache._spaces.values():
+        assert not space[1].any()
     return out, lse, worst
 
 

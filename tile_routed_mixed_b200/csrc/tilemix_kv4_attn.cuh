@@ -13,18 +13,19 @@
 // as a tile's arithmetic stays under its transfer time, about 180 cycles of an
 // SM for the 4.2 KB of a tile.  What has to be short is the way from 4 bits to
 // an operand of the matrix product:
-//   - codes are stored as u = code + 8, and a nibble in the top four of an
-//     fp16's ten significand bits, exponent field 0, is the subnormal u 2^-18,
-//     an exact operand as it stands: a shift and an AND per pair of codes, no
-//     conversion, no subtraction.  (At bits 0 and 4 two of the four shifts fall
-//     away, but the products are aligned by the subnormals' exponent, 2^-14, not
-//     by their leading bit, before they are added: sums then lose six more
-//     bits, measured as errors of 1e-4 of a code.);
+//   - codes are stored as u = code + 8: a nibble in the low bits of an fp16
+//     whose exponent field is that of 1024 makes it 1024 + u (one three-input
+//     logic operation), and one packed addition leaves the code itself, an exact
+//     integer; a nibble four bits up makes 1024 + 16 u, and the packed
+//     multiply-add by 1/16 does as much.  Nine instructions for eight codes.
+//     (Masked nibbles are also exact operands as they stand, as fp16
+//     subnormals, at five instructions or eight.  But then 8 sum(P) has to come
+//     off sums that are large against the result: over 16,000 keys a warp, with
+//     the truncation in the products' sums, that cost a factor of three in O's
+//     error; and at five instructions products are aligned by the subnormals'
+//     exponent and lose six bits more.)
 //   - keys are the rows (M = 16) of both products, queries the 8 columns, so
 //     that no row is padding: S^T = K Q^T, and O^T = V^T P^T;
-//   - the offset 8 leaves as 8 sum(q) per column from each score and as
-//     8 sum(P) per column from each output; sum(P) comes from a product with
-//     ones, in the layout of the outputs.
 // Q is scaled per column by a power of two, so its largest magnitude is near
 // 2^14 and every channel keeps at least 11 bits (fp16 has 5 of exponent,
 // bf16 has 8) down to 2^-28 of it.  K's scales multiply the scores, V's the
@@ -77,11 +78,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Nibble I of both halves of x as two fp16 subnormals u 2^-18.
-template <int I>
-__device__ __forceinline__ uint32_t nibble(uint32_t x) {
-  constexpr int by = 6 - 4 * I;
-  return (by >= 0 ? x << (by >= 0 ? by : 0) : x >> (by < 0 ? -by : 0)) & 0x03C003C0u;
+// The codes of nibbles I (0: the low one) of both halves of a word, as fp16.
+__device__ __forceinline__ uint32_t or_1024(uint32_t x, uint32_t mask) {  // (x & mask) | 0x64006400
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(x), "r"(mask));
+  return y;
+}
+__device__ __forceinline__ uint32_t code_low(uint32_t x) {  // bits 0 .. 3: 1024 + u - 1032
+  uint32_t y = or_1024(x, 0x000F000Fu);
+  asm("add.f16x2 %0, %0, %1;" : "+r"(y) : "r"(0xE408E408u));
+  return y;
+}
+__device__ __forceinline__ uint32_t code_high(uint32_t x) {  // bits 4 .. 7: (1024 + 16 u) / 16 - 72
+  uint32_t y = or_1024(x, 0x00F000F0u);
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x2C002C00u), "r"(0xD480D480u));
+  return y;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -330,7 +341,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const bool whole = cur.t == 0 && n == cur.w.tiles;
       const bool head = !whole && n < left;  // more tiles of this warp follow
       uint32_t qf[NB][kT][4];
-      float cs[NB][2], corr[NB][2][kNg];
+      float cs[NB][2];  // scale of a column's scores, log2 units
       int lim[NB][2];  // keys that each column sees
       const int seen0 = cur.w.len - cur.w.queries + 1;  // ... of query token 0
       const int min_lim =
@@ -355,9 +366,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t fe = (am == 0 || am >= kv4::kInfBits<BF16>) ? 127u : min(268u - ex, 253u);
         const float f = __uint_as_float(fe << 23);
         const float inv_f = __uint_as_float((254u - fe) << 23);
-        float sums[kNg];
-#pragma unroll
-        for (int i = 0; i < kNg; ++i) sums[i] = 0.f;
 #pragma unroll
         for (int t = 0; t < kT; ++t) {
           const float2 c01 = kv4::unpack2<BF16>(x[t].x), c23 = kv4::unpack2<BF16>(x[t].y);
@@ -366,30 +374,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           qf[nb][t][1] = kv4::pack2<false>(c23.x * f, c67.x * f);
           qf[nb][t][2] = kv4::pack2<false>(c01.y * f, c45.y * f);
           qf[nb][t][3] = kv4::pack2<false>(c23.y * f, c67.y * f);
-          const float2 e0 = kv4::unpack2<false>(qf[nb][t][0]), e1 = kv4::unpack2<false>(qf[nb][t][1]);
-          const float2 o0 = kv4::unpack2<false>(qf[nb][t][2]), o1 = kv4::unpack2<false>(qf[nb][t][3]);
-          sums[t / kTg] += ((e0.x + e0.y) + (e1.x + e1.y)) + ((o0.x + o0.y) + (o1.x + o1.y));
         }
         const float unit = inv_f * p.scale_log2;
 #pragma unroll
-        for (int i = 0; i < kNg; ++i) {
-          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 1);
-          sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], 2);
-          sums[i] *= 8.0f * unit;
-        }
-#pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int from = (2 * q4 + j) * 4;  // a lane of that column
-          cs[nb][j] = __shfl_sync(0xffffffffu, unit, from) * 0x1p18f;
-#pragma unroll
-          for (int i = 0; i < kNg; ++i) corr[nb][j][i] = __shfl_sync(0xffffffffu, sums[i], from);
+          cs[nb][j] = __shfl_sync(0xffffffffu, unit, from);
           const int tk = __shfl_sync(0xffffffffu, tok, from);
           lim[nb][j] = tk < cur.w.queries ? seen0 + tk : cur.w.len;
         }
       }
 
       // ---- its running state ----
-      float o[kT][2][NB][4], ps[kNg][NB][4];
+      float o[kT][2][NB][4];
       float m[NB][2], mu[NB][2], l[NB][2];
       float sig = 0x1p-100f, vmul = 0x1p105f;  // V's power of two, 2^5 over it
 #pragma unroll
@@ -400,10 +397,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[t][i][nb][c] = 0.f;
-#pragma unroll
-        for (int i = 0; i < kNg; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) ps[i][nb][c] = 0.f;
         m[nb][0] = m[nb][1] = -INFINITY;
         mu[nb][0] = mu[nb][1] = 0.f;
         l[nb][0] = l[nb][1] = 0.f;
@@ -469,10 +462,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
               const uint32_t x = k0[t], y = k1[t];
-              const uint32_t ev[4] = {kv4::nibble<0>(x), kv4::nibble<0>(y), kv4::nibble<2>(x),
-                                      kv4::nibble<2>(y)};
-              const uint32_t od[4] = {kv4::nibble<1>(x), kv4::nibble<1>(y), kv4::nibble<3>(x),
-                                      kv4::nibble<3>(y)};
+              const uint32_t xh = x >> 8, yh = y >> 8;
+              const uint32_t ev[4] = {kv4::code_low(x), kv4::code_low(y), kv4::code_low(xh),
+                                      kv4::code_low(yh)};
+              const uint32_t od[4] = {kv4::code_high(x), kv4::code_high(y), kv4::code_high(xh),
+                                      kv4::code_high(yh)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 dec::mma_f16(acc[nb], ev, qf[nb][t][0], qf[nb][t][1]);
@@ -485,11 +479,14 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                s[mb][nb][j] = fmaf(fmaf(acc[nb][j], cs[nb][j], -corr[nb][j][i]), a0, s[mb][nb][j]);
-                s[mb][nb][2 + j] =
-                    fmaf(fmaf(acc[nb][2 + j], cs[nb][j], -corr[nb][j][i]), a1, s[mb][nb][2 + j]);
+                s[mb][nb][j] = fmaf(acc[nb][j], a0, s[mb][nb][j]);
+                s[mb][nb][2 + j] = fmaf(acc[nb][2 + j], a1, s[mb][nb][2 + j]);
               }
           }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[mb][nb][c] *= cs[nb][c & 1];
         }
         if (key0 + kAttnKeys > min_lim) {
           // keys that a column does not see; rows past the cache hold whatever
@@ -555,11 +552,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                   o[t][i][nb][j] *= ao;
                   o[t][i][nb][2 + j] *= ao;
                 }
-#pragma unroll
-              for (int i = 0; i < kNg; ++i) {
-                ps[i][nb][j] *= ao;
-                ps[i][nb][2 + j] *= ao;
-              }
             }
         }
 
@@ -592,12 +584,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const float f1 =
                 vmul * kv4::unpack1<BF16>((i & 1) ? vsc[mb][1][i / 2] >> 16 : vsc[mb][1][i / 2] & 0xffffu);
             uint32_t pb[NB][2];
-            const uint32_t ones[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               pb[nb][0] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][0] * f0, s[mb][nb][1] * f0));
               pb[nb][1] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][2] * f1, s[mb][nb][3] * f1));
-              dec::mma_f16(ps[i][nb], ones, pb[nb][0], pb[nb][1]);
             }
 #pragma unroll
             for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
@@ -605,10 +595,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
               const uint32_t pick = (t & 1) ? 0x7632u : 0x5410u;
               const uint32_t x = __byte_perm(v[0][t / 2], v[1][t / 2], pick);
               const uint32_t y = __byte_perm(v[2][t / 2], v[3][t / 2], pick);
-              const uint32_t ev[4] = {kv4::nibble<0>(x), kv4::nibble<2>(x), kv4::nibble<0>(y),
-                                      kv4::nibble<2>(y)};
-              const uint32_t od[4] = {kv4::nibble<1>(x), kv4::nibble<3>(x), kv4::nibble<1>(y),
-                                      kv4::nibble<3>(y)};
+              const uint32_t xh = x >> 8, yh = y >> 8;
+              const uint32_t ev[4] = {kv4::code_low(x), kv4::code_low(xh), kv4::code_low(y),
+                                      kv4::code_low(yh)};
+              const uint32_t od[4] = {kv4::code_high(x), kv4::code_high(xh), kv4::code_high(y),
+                                      kv4::code_high(yh)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 dec::mma_f16(o[t][0][nb], ev, pb[nb][0], pb[nb][1]);
@@ -643,12 +634,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const float down = whole ? (lsum == 0.f ? 0.f : 0.03125f * sig / lsum) : 0.03125f * sig;
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
-            const float off = 8.0f * ps[t / kTg][nb][j];
             float4 x;
-            x.x = fmaf(o[t][0][nb][j], 0x1p18f, -off) * down;
-            x.y = fmaf(o[t][1][nb][j], 0x1p18f, -off) * down;
-            x.z = fmaf(o[t][0][nb][2 + j], 0x1p18f, -off) * down;
-            x.w = fmaf(o[t][1][nb][2 + j], 0x1p18f, -off) * down;
+            x.x = o[t][0][nb][j] * down;
+            x.y = o[t][1][nb][j] * down;
+            x.z = o[t][0][nb][2 + j] * down;
+            x.w = o[t][1][nb][2 + j] * down;
             const int ch = 32 * t + 4 * g;
             if (!whole)
               *reinterpret_cast<float4*>(part + col * D + ch) = x;

@@ -12,13 +12,13 @@ and none of it reads anything back to the host.
 """
 from __future__ import annotations
 
+import ctypes
 from typing import NamedTuple
 
 import torch
 
 from . import (KV_DTYPES, KV4_SYNC_WORDS, KV4AppendArgs, KV4AttnArgs, KV4Cache, KV4GatherArgs,
-               PagePlanArgs, lib, tilemix_kv4_append, tilemix_kv4_attn,
-               tilemix_kv4_attn_workspace_size, tilemix_kv4_gather, tilemix_page_plan)
+               PagePlanArgs, _check, lib, tilemix_kv4_attn_workspace_size)
 
 
 class PagePlan(NamedTuple):
@@ -55,7 +55,7 @@ class TileMixKV4Cache:
 
     def __init__(self, num_pages, page_size, hk, d, max_seqs, max_pages, group=32,
                  dtype=torch.float16, device="cuda", pool=None, tables=None):
-        lib()
+        L = lib()
         self.num_pages, self.page_size = int(num_pages), int(page_size)
         self.hk, self.d, self.group = int(hk), int(d), int(group)
         self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
@@ -69,6 +69,7 @@ class TileMixKV4Cache:
             raise ValueError("sizes start at 1")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         dev, i32 = self.device, torch.int32
         rows = (self.num_pages, self.hk, self.page_size)
         shapes = [(rows + (self.d // 2,), torch.uint8), (rows + (self.d // self.group,), dtype)] * 2
@@ -103,16 +104,27 @@ class TileMixKV4Cache:
         self._gather.block_table, self._gather.seq_len = self.block_table.data_ptr(), self.seq_len.data_ptr()
         self._attn = KV4AttnArgs(cache=c, max_pages=self.max_pages)
         self._attn.block_table, self._attn.seq_len = self.block_table.data_ptr(), self.seq_len.data_ptr()
+        # a step's calls are a few microseconds of host time each: the argument
+        # blocks and the functions are kept
+        self._calls = {
+            "tilemix_page_plan": (L.tilemix_page_plan, ctypes.byref(self._plan)),
+            "tilemix_kv4_append": (L.tilemix_kv4_append, ctypes.byref(self._append)),
+            "tilemix_kv4_gather": (L.tilemix_kv4_gather, ctypes.byref(self._gather)),
+            "tilemix_kv4_attn": (L.tilemix_kv4_attn, ctypes.byref(self._attn)),
+        }
         self._spaces = {}
 
     # ---------------------------------------------------------------- checks
 
     def _expect(self, x, dtype, shape, what):
         """x is a contiguous tensor of this device; a None in shape matches any size."""
-        if x.dtype != dtype or x.device != self.device or not x.is_contiguous() or \
-                x.dim() != len(shape) or any(n is not None and a != n for a, n in zip(x.shape, shape)):
-            raise ValueError("%s: expected a contiguous %s tensor of shape %s on %s, got %s %s on %s"
-                             % (what, dtype, tuple(shape), self.device, x.dtype, tuple(x.shape), x.device))
+        if x.dtype is dtype and x.get_device() == self._index and x.is_contiguous():
+            have = x.shape
+            if have == shape or (len(have) == len(shape) and
+                                 all(n is None or a == n for a, n in zip(have, shape))):
+                return
+        raise ValueError("%s: expected a contiguous %s tensor of shape %s on %s, got %s %s on %s"
+                         % (what, dtype, tuple(shape), self.device, x.dtype, tuple(x.shape), x.device))
 
     def _nseq(self, x, what, extra=0):
         n = x.shape[0] - extra
@@ -121,16 +133,23 @@ class TileMixKV4Cache:
         return n
 
     def _on(self, stream, fn, *args):
-        """fn(*args) with this object's device, and `stream`, current."""
+        """fn(*args, raw stream) with this object's device, and `stream`, current."""
         if stream is not None:
             if stream.device != self.device:
                 raise ValueError("the stream belongs to %s, the cache to %s" % (stream.device, self.device))
             with torch.cuda.stream(stream):
-                return fn(*args)
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
-                return fn(*args)
-        return fn(*args)
+                return fn(*args, stream.cuda_stream)
+        index = self._index
+        if torch.cuda.current_device() != index:
+            with torch.cuda.device(index):
+                return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+        return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+
+    def _call(self, name, stream):
+        fn, args = self._calls[name]
+        rc = fn(args, stream)
+        if rc:
+            _check(rc, name)
 
     # ----------------------------------------------------------------- calls
 
@@ -146,7 +165,7 @@ class TileMixKV4Cache:
         max_tokens: the number of slots, or `out` from new_plan()."""
         return self._on(stream, self._plan_call, new_len, max_tokens, out)
 
-    def _plan_call(self, new_len, max_tokens, out):
+    def _plan_call(self, new_len, max_tokens, out, stream):
         n = self._nseq(new_len, "new_len")
         self._expect(new_len, torch.int32, (n,), "new_len")
         if out is None:
@@ -165,7 +184,7 @@ class TileMixKV4Cache:
         a.slots, a.max_tokens = out.slots.data_ptr(), out.slots.shape[0]
         if n == 0:  # an empty tensor has no address
             a.new_len = a.granted = out.token_start.data_ptr()
-        tilemix_page_plan(a)
+        self._call("tilemix_page_plan", stream)
         return out
 
     def append(self, k, v, slots, stream=None):
@@ -173,24 +192,28 @@ class TileMixKV4Cache:
         any stride) to slots [n] (int32; -1: skipped)."""
         return self._on(stream, self._append_call, k, v, slots)
 
-    def _append_call(self, k, v, slots):
+    def _append_call(self, k, v, slots, stream):
         n = slots.shape[0]
         self._expect(slots, torch.int32, (n,), "slots")
         a = self._append
-        for x, what in ((k, "k"), (v, "v")):
-            if x.dtype != self.dtype or x.device != self.device or x.dim() != 3 or \
-                    x.shape[0] < n or x.shape[1] != self.hk or x.shape[2] != self.d:
-                raise ValueError("%s: expected %s [%d or more, %d, %d] on %s" %
-                                 (what, self.dtype, n, self.hk, self.d, self.device))
-            if x.stride(2) != 1 or (self.hk > 1 and x.stride(1) != self.d):
-                raise ValueError("%s: a token's heads must be contiguous" % what)
+        a.k_stride, a.v_stride = self._rows(k, n, "k"), self._rows(v, n, "v")
         if n == 0:
             return
-        row = self.hk * self.d
         a.k, a.v, a.slots, a.n = k.data_ptr(), v.data_ptr(), slots.data_ptr(), n
-        a.k_stride = k.stride(0) if k.shape[0] > 1 else row
-        a.v_stride = v.stride(0) if v.shape[0] > 1 else row
-        tilemix_kv4_append(a)
+        self._call("tilemix_kv4_append", stream)
+
+    def _rows(self, x, n, what):
+        """The stride of x's tokens."""
+        shape = x.shape
+        if x.dtype is not self.dtype or x.get_device() != self._index or len(shape) != 3 or \
+                shape[0] < n or shape[1] != self.hk or shape[2] != self.d:
+            raise ValueError("%s: expected %s [%d or more, %d, %d] on %s, got %s %s on %s" %
+                             (what, self.dtype, n, self.hk, self.d, self.device, x.dtype,
+                              tuple(shape), x.device))
+        token, head, channel = x.stride()
+        if channel != 1 or (self.hk > 1 and head != self.d):
+            raise ValueError("%s: a token's heads must be contiguous" % what)
+        return token if shape[0] > 1 else self.hk * self.d
 
     def gather(self, out_start, rows, out=None, stream=None):
         """K and V of the sequences' tokens as 16-bit values: position p of
@@ -198,7 +221,7 @@ class TileMixKV4Cache:
         tensors (`out`, or new ones)."""
         return self._on(stream, self._gather_call, out_start, rows, out)
 
-    def _gather_call(self, out_start, rows, out):
+    def _gather_call(self, out_start, rows, out, stream):
         n = self._nseq(out_start, "out_start")
         self._expect(out_start, torch.int32, (n,), "out_start")
         rows = int(rows)
@@ -212,7 +235,7 @@ class TileMixKV4Cache:
         a = self._gather
         a.out_start, a.nseq, a.rows = out_start.data_ptr(), n, rows
         a.k, a.v = out[0].data_ptr(), out[1].data_ptr()
-        tilemix_kv4_gather(a)
+        self._call("tilemix_kv4_gather", stream)
         return tuple(out)
 
     def attend(self, q, max_seqlen, token_start=None, max_new=1, softmax_scale=0.0, out=None,
@@ -227,7 +250,7 @@ class TileMixKV4Cache:
         return self._on(stream, self._attend_call, q, max_seqlen, token_start, max_new,
                         softmax_scale, out, lse)
 
-    def _attend_call(self, q, max_seqlen, token_start, max_new, softmax_scale, out, lse):
+    def _attend_call(self, q, max_seqlen, token_start, max_new, softmax_scale, out, lse, stream):
         self._expect(q, self.dtype, (None, None, self.d), "q")
         rows, hq = q.shape[0], q.shape[1]
         if hq < 1 or hq % self.hk != 0:
@@ -254,25 +277,22 @@ class TileMixKV4Cache:
         a.nseq, a.total_q, a.hq = n, rows, hq
         a.max_new, a.max_seqlen, a.softmax_scale = int(max_new), int(max_seqlen), float(softmax_scale)
         if rows and n:
-            space = self._space(a)
-            a.workspace, a.workspace_bytes = space[0].data_ptr(), space[0].shape[0]
-            a.sync = space[1].data_ptr()
-        tilemix_kv4_attn(a)
+            # kept until the call is enqueued: a graph's own lives in its pool from then on
+            work, sync, a.workspace, a.workspace_bytes, a.sync = self._space(a, stream)
+            self._call("tilemix_kv4_attn", stream)
         return (out, lse) if want else out
 
-    def _space(self, a):
-        """(workspace, sync words) of the current stream."""
-        key = torch.cuda.current_stream().cuda_stream
-        if torch.cuda.is_current_stream_capturing():
-            # a graph's own: its replays must not share one with calls outside it
-            nbytes = tilemix_kv4_attn_workspace_size(a)
-            return (torch.empty(nbytes, dtype=torch.uint8, device=self.device),
-                    torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device))
-        cols = a.max_new * a.hq > 8 * self.hk
-        space = self._spaces.get((key, cols))
-        if space is None:
-            nbytes = tilemix_kv4_attn_workspace_size(a)
-            space = (torch.empty(nbytes, dtype=torch.uint8, device=self.device),
-                     torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device))
-            self._spaces[(key, cols)] = space
+    def _space(self, a, stream):
+        """Workspace and sync words of a stream, and their addresses and size."""
+        key = (stream, a.max_new * a.hq > 8 * self.hk)
+        space = self._spaces.get(key)
+        if space is not None and not torch.cuda.is_current_stream_capturing():
+            return space
+        # a graph being captured gets one of its own: its replays must not share
+        # one with calls outside it
+        work = torch.empty(tilemix_kv4_attn_workspace_size(a), dtype=torch.uint8, device=self.device)
+        sync = torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device)
+        space = (work, sync, work.data_ptr(), work.shape[0], sync.data_ptr())
+        if not torch.cuda.is_current_stream_capturing():
+            self._spaces[key] = space
         return space

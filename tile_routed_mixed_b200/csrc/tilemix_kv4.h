@@ -77,7 +77,7 @@ int launch_kv4_gather(const Kv4GatherParams& p, const Kv4Format& f, cudaStream_t
 struct Kv4AttnShape {
   int ctas, warps, cols;
 };
-Kv4AttnShape kv4_attn_shape(const Kv4Format& f, int sms, long long columns);
+Kv4AttnShape kv4_attn_shape(int sms, long long columns);
 int launch_kv4_attn(const Kv4AttnParams& p, const Kv4Format& f, const Kv4AttnShape& shape,
                     cudaStream_t stream);
 int kv4_read_and_clear_status(unsigned int* status);

@@ -29,9 +29,11 @@
 // Q is scaled per column by a power of two, so its largest magnitude is near
 // 2^14 and every channel keeps at least 11 bits (fp16 has 5 of exponent,
 // bf16 has 8) down to 2^-28 of it.  K's scales multiply the scores, V's the
-// probabilities: P s_v, over a running power of two near the largest V
-// scale, is what is rounded to fp16.  The running maximum moves only when a
-// score passes it by 2^8: P s_v stays below 2^14, and fp32 holds the sums.
+// probabilities: P s_v is what is rounded to fp16.  A column's probabilities are
+// 2^(score - r) with r = the largest score + log2 of the largest V scale (its
+// power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
+// a score passes the old largest by 8 or a scale doubles: P s_v stays below
+// 2^14, and fp32 holds the sums.  r cancels between O and the sum.
 //
 // Layouts.  With MMA fragments (rows g and g + 8, column pairs q4) a lane's
 // operands of K are D / 32 words of a key's row, 16 (or 8) bytes together in
@@ -44,32 +46,42 @@
 
 namespace tilemix {
 
-constexpr int kAttnWarps = 8;
-constexpr int kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnKeys = 32;      // keys of a tile
+constexpr int kAttnKeys = 32;  // keys of a tile
+
+// Warps of a CTA (one CTA per SM), by column blocks: a warp's state and
+// operands fit 128 registers with 8 columns, 255 with 16.
+template <int NB>
+constexpr int kAttnWarps = NB == 1 ? 16 : 8;
+constexpr int kAttnMaxCtas = 160;  // at least one per SM (148 on a B200)
 constexpr int kAttnMinTiles = 16;  // tiles a CTA takes at least, while there are any
 
-template <int D, int GROUP>
+template <int D, int GROUP, int NB>
 struct AttnTile {
   static constexpr int kNg = D / GROUP;                 // scales per row
   static constexpr int kT = D / 32;                     // 32-channel chunks of a row
   static constexpr int kCodes = kAttnKeys * D / 2;      // bytes of K's (and V's) codes
   static constexpr int kScales = kAttnKeys * 2 * kNg;   // ... and scales
   static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kRowBytes = D + 4 * kNg;         // of one key, K and V
   static constexpr int kOffV = kCodes;
   static constexpr int kOffKs = 2 * kCodes;
   static constexpr int kOffVs = 2 * kCodes + kScales;
-  // as many stages as fit beside the merge's weights, at most six
-  static constexpr int kStages = 200 * 1024 / (kAttnWarps * kBytes) > 6
-                                     ? 6
-                                     : 200 * 1024 / (kAttnWarps * kBytes);
+  // as many stages as fit beside the merge's weights and 4 KB of the kernel's own,
+  // at most six
+  static constexpr int kWeights = kAttnMaxCtas * 8 * NB * 4;
+  static constexpr int kFit = (223 * 1024 - kWeights) / (kAttnWarps<NB> * kBytes);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static_assert(kStages >= 3, "ring too short");
+  static_assert(kStages * kBytes >= 8 * NB * (D + 2) * 4, "a partial state fits a warp's ring");
 };
 
 namespace kv4 {
 
+// 16 bytes from global to shared memory; off, a byte offset, is added to both.
+template <int OFF_DST, int OFF_SRC>
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0 + %2], [%1 + %3], 16;" ::"r"(dst), "l"(src),
+               "n"(OFF_DST), "n"(OFF_SRC)
                : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -93,6 +105,30 @@ __device__ __forceinline__ uint32_t code_high(uint32_t x) {  // bits 4 .. 7: (10
   uint32_t y = or_1024(x, 0x00F000F0u);
   asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x2C002C00u), "r"(0xD480D480u));
   return y;
+}
+
+// D[16x8] = A[16x16] * B[16x8], fp16 inputs, fp32 sums from zero.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Larger magnitude-ordered half of two packed non-negative values (NaNs drop out).
+template <bool BF16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  } else {
+    const __half2 m =
+        __hmax2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -172,18 +208,18 @@ struct Cursor {
     t = static_cast<int>(off - static_cast<long long>(u) * w.tiles);
     enter_unit(p);
   }
-  // To the first tile of the next unit; false past the last one.
-  __device__ __forceinline__ bool next_unit(const Kv4AttnParams& p) {
+  // To the first tile of the next unit; there is one.
+  __device__ __forceinline__ void next_unit(const Kv4AttnParams& p) {
     t = 0;
     if (++u == p.pool.hk * w.blocks) {
       u = 0;
       do {
-        if (++s >= p.nseq) return false;
+        s = min(s + 1, p.nseq - 1);
         w = seq_work<NB>(p, s);
-      } while (w.blocks == 0);
+      } while (w.blocks == 0 && s + 1 < p.nseq);
+      w.blocks = max(w.blocks, 1);
     }
     enter_unit(p);
-    return true;
   }
 };
 
@@ -201,18 +237,21 @@ struct Part {
 }  // namespace kv4
 
 template <int D, int GROUP, int NB, bool BF16>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
-  using Tile = AttnTile<D, GROUP>;
+  using Tile = AttnTile<D, GROUP, NB>;
+  constexpr int kWarps = kAttnWarps<NB>, kThreads = 32 * kWarps;
   constexpr int kNg = Tile::kNg, kT = Tile::kT, kStages = Tile::kStages;
   constexpr int kCols = 8 * NB;
   constexpr int kTg = kT / kNg;  // chunks per scale group
   extern __shared__ __align__(128) uint8_t attn_smem[];
-  __shared__ long long warp_tiles[kAttnWarps];
-  __shared__ int start_seq[kAttnWarps];
-  __shared__ long long start_off[kAttnWarps];
-  __shared__ kv4::Part parts[2 * kAttnWarps];
-  __shared__ float* run[2 * kAttnWarps];
+  __shared__ long long warp_tiles[kWarps];
+  __shared__ int warp_units[kWarps];
+  __shared__ int start_seq[kWarps];
+  __shared__ long long start_off[kWarps];
+  __shared__ kv4::Cursor<NB> cursors[2 * kWarps];
+  __shared__ kv4::Part parts[2 * kWarps];
+  __shared__ float* run[2 * kWarps];
   __shared__ float top[kCols], sum[kCols];
   __shared__ int merge_last;
 
@@ -220,32 +259,53 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int g = lane >> 2, q4 = lane & 3;
 
   // ---- the schedule: this CTA's tiles [a, b), this warp's [wa, wb) ----
-  const int per = (p.nseq + kAttnThreads - 1) / kAttnThreads;
+  const int per = (p.nseq + kThreads - 1) / kThreads;
   const int s0 = min(p.nseq, tid * per), s1 = min(p.nseq, s0 + per);
   long long mine = 0;
-  for (int s = s0; s < s1; ++s) mine += kv4::seq_tiles(p, kv4::seq_work<NB>(p, s));
+  int units = 0;
+  for (int s = s0; s < s1; ++s) {
+    const kv4::SeqWork w = kv4::seq_work<NB>(p, s);
+    mine += kv4::seq_tiles(p, w);
+    units = min(units + min(p.pool.hk * w.blocks, 0xffff), 0xffff);  // all that matters: fewer than CTAs?
+  }
   long long inc = mine;
 #pragma unroll
   for (int by = 1; by < 32; by <<= 1) {
     const long long up = __shfl_up_sync(0xffffffffu, inc, by);
     if (lane >= by) inc += up;
   }
-  if (lane == 31) warp_tiles[warp] = inc;
-  if (tid < 2 * kAttnWarps) parts[tid].at = nullptr;
+  units = __reduce_add_sync(0xffffffffu, units);
+  if (lane == 31) {
+    warp_tiles[warp] = inc;
+    warp_units[warp] = units;
+  }
+  if (tid < 2 * kWarps) parts[tid].at = nullptr;
   __syncthreads();
   long long base = inc - mine, total = 0;
+  units = 0;
 #pragma unroll
-  for (int w = 0; w < kAttnWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     if (w < warp) base += warp_tiles[w];
     total += warp_tiles[w];
+    units += warp_units[w];
   }
-  const long long most = (total + kAttnMinTiles - 1) / kAttnMinTiles;
-  const long long ctas = most < gridDim.x ? most : gridDim.x;
-  if (static_cast<long long>(blockIdx.x) >= ctas) return;
-  const long long a = blockIdx.x * total / ctas, b = (blockIdx.x + 1) * total / ctas;
-  const auto warp_begin = [&](int w) { return a + (b - a) * w / kAttnWarps; };
+  // CTAs that take part.  With fewer units than CTAs each unit gets the same
+  // number of them (units of one length are then cut at their own ends, and
+  // none shares a CTA); otherwise the ranges go where they fall.
+  int ctas = gridDim.x;
+  if (units < ctas) {
+    const long long each = total / (static_cast<long long>(max(units, 1)) * kAttnMinTiles);
+    ctas = units * static_cast<int>(max(1LL, min(each, static_cast<long long>(ctas / max(units, 1)))));
+  }
+  if (static_cast<int>(blockIdx.x) >= ctas) return;
+  const auto cta_begin = [&](int c) {
+    return static_cast<long long>(static_cast<unsigned long long>(c) * total /
+                                  static_cast<unsigned>(ctas));
+  };
+  const long long a = cta_begin(blockIdx.x), b = cta_begin(blockIdx.x + 1);
+  const auto warp_begin = [&](int w) { return a + (b - a) * w / kWarps; };
 #pragma unroll 1
-  for (int w = 0; w < kAttnWarps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     const long long x = warp_begin(w);
     if (x >= base && x < base + mine) {
       long long off = x - base;
@@ -265,61 +325,104 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // ---- this warp's tiles ----
   if (wa < wb) {
     uint8_t* ring = attn_smem + warp * (kStages * Tile::kBytes);
-    const uint32_t ring_addr = ptx::smem_addr(ring);
-    kv4::Cursor<NB> in;  // the next tile to fetch
-    in.start(p, start_seq[warp], start_off[warp]);
-    kv4::Cursor<NB> cur = in;
-    long long to_issue = wb - wa;
+    // the next tile to fetch, and the unit being computed: kept in shared memory
+    // but for what a tile needs
+    kv4::Cursor<NB>& in = cursors[2 * warp];
+    kv4::Cursor<NB>& cur = cursors[2 * warp + 1];
+    {
+      kv4::Cursor<NB> c;
+      c.start(p, start_seq[warp], start_off[warp]);
+      if (lane == 0) in = cur = c;
+      __syncwarp();
+    }
     const int page_sh = p.pool.page_shift, page_1 = (1 << page_sh) - 1;
+    const int count = static_cast<int>(wb - wa);
+    int issued = 0;
+    // Copies of a tile, 16 bytes a lane: each half of K's and V's codes (16 keys,
+    // within one page) is D / 64 rounds of the warp, all four parts of the
+    // scales together are one.
+    // V's 16-byte chunks of a 64-byte row are exchanged by bit 2 of the key.
+    const uint32_t dst0 = ptx::smem_addr(ring) + lane * 16;
+    const uint32_t dstv0 = ptx::smem_addr(ring) + Tile::kOffV +
+                           (D == 128 ? (lane * 16) ^ ((lane & 16) << 1) : lane * 16);
+    const int64_t v_minus_k = p.pool.v_codes - p.pool.k_codes;
+    const int sc_half = (lane / (2 * kNg)) & 1;
+    const uint8_t* sc_src = (lane < 4 * kNg ? p.pool.k_scale : p.pool.v_scale) + (lane % (2 * kNg)) * 16;
+    int in_t = in.t, in_keys = in.keys, in_tiles = in.w.tiles, in_kv = in.kv;
+    const int32_t* in_table = p.block_table + static_cast<size_t>(in.s) * p.max_pages;
+    int page_next = in_t * kAttnKeys < in_keys ? __ldg(in_table + ((in_t * kAttnKeys) >> page_sh)) : 0;
+    // Tiles are fetched in runs: tiles of one page, or (run_reads false) tiles
+    // that no column sees, which are passed over.  A run's sources: this lane's
+    // 16 bytes of the first and second sixteen keys of K, and of the scales.
+    int run = 0;
+    bool run_reads = false;
+    const uint8_t *k_lo = nullptr, *k_hi = nullptr, *sc = nullptr;
+    const auto next_run = [&]() {
+      if (in_t == in_tiles) {
+        kv4::Cursor<NB> c = in;
+        c.next_unit(p);
+        __syncwarp();
+        if (lane == 0) in = c;
+        __syncwarp();
+        in_t = 0, in_keys = c.keys, in_tiles = c.w.tiles, in_kv = c.kv;
+        in_table = p.block_table + static_cast<size_t>(c.s) * p.max_pages;
+        page_next = in_keys > 0 ? __ldg(in_table) : 0;
+      }
+      const int key = in_t * kAttnKeys;
+      run_reads = key < in_keys;
+      if (!run_reads) {
+        run = in_tiles - in_t;
+        in_t = in_tiles;
+        return;
+      }
+      // a page outside the pool is reported, and page 0 read in its place
+      int lo = page_next, hi = page_next;
+      if (page_sh == 4) {
+        // two pages; the second sixteen may have no key to see: then the first again
+        run = 1;
+        if (key + 16 < in_keys) hi = __ldg(in_table + (key >> 4) + 1);
+      } else {
+        run = min((page_1 + 1 - (key & page_1)) / kAttnKeys, (in_keys - key + kAttnKeys - 1) / kAttnKeys);
+      }
+      if (static_cast<unsigned>(lo) >= static_cast<unsigned>(p.pool.num_pages) ||
+          static_cast<unsigned>(hi) >= static_cast<unsigned>(p.pool.num_pages)) {
+        atomicOr(&g_kv4_status, kStatusBadPages);
+        lo = hi = 0;
+      }
+      const size_t row_lo = ((static_cast<size_t>(lo) * p.pool.hk + in_kv) << page_sh) + (key & page_1);
+      const size_t row_hi = page_sh == 4 ? (static_cast<size_t>(hi) * p.pool.hk + in_kv) << 4 : row_lo + 16;
+      k_lo = p.pool.k_codes + row_lo * (D / 2) + lane * 16;
+      k_hi = p.pool.k_codes + row_hi * (D / 2) + lane * 16;
+      sc = sc_src + (sc_half ? row_hi : row_lo) * (2 * kNg);
+      in_t += run;
+      const int then = in_t * kAttnKeys;
+      if (then < in_keys) page_next = __ldg(in_table + (then >> page_sh));
+    };
 
-    // Fetches tile `in` into `stage` and moves on.  Keys come in two halves of
-    // 16, each within one page; a half that no column sees is not fetched.
+    // Fetches the next tile into `stage`.
     const auto issue = [&](int stage) {
-      if (to_issue > 0) {
-        --to_issue;
-        const int key0 = in.t * kAttnKeys;
-        if (key0 < in.keys) {
-          const int32_t* table = p.block_table + static_cast<size_t>(in.s) * p.max_pages;
-          const uint32_t dst = ring_addr + stage * Tile::kBytes;
-          size_t row[2];
-          bool on[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int key = key0 + 16 * h;
-            on[h] = key < in.keys;
-            const int page = on[h] ? __ldg(table + (key >> page_sh)) : 0;
-            if (page < 0 || page >= p.pool.num_pages) {
-              on[h] = false;
-              atomicOr(&g_kv4_status, kStatusBadPages);
-            }
-            row[h] = ((static_cast<size_t>(page) * p.pool.hk + in.kv) << page_sh) + (key & page_1);
+      if (issued < count) {
+        ++issued;
+        if (run == 0) next_run();
+        --run;
+        if (run_reads) {
+          const uint32_t dst = dst0 + stage * Tile::kBytes, dstv = dstv0 + stage * Tile::kBytes;
+          kv4::cp16<0, 0>(dst, k_lo);
+          kv4::cp16<0, 0>(dstv, k_lo + v_minus_k);
+          kv4::cp16<8 * D, 0>(dst, k_hi);
+          kv4::cp16<8 * D, 0>(dstv, k_hi + v_minus_k);
+          if constexpr (D == 128) {
+            kv4::cp16<512, 512>(dst, k_lo);
+            kv4::cp16<512, 512>(dstv, k_lo + v_minus_k);
+            kv4::cp16<8 * D + 512, 512>(dst, k_hi);
+            kv4::cp16<8 * D + 512, 512>(dstv, k_hi + v_minus_k);
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (on[h]) {
-              const uint8_t* ks = p.pool.k_codes + row[h] * (D / 2);
-              const uint8_t* vs = p.pool.v_codes + row[h] * (D / 2);
-#pragma unroll
-              for (int i = 0; i < D / 64; ++i) {
-                const int c = lane + 32 * i;  // 16-byte chunk of the half
-                const uint32_t at = dst + h * (8 * D);
-                kv4::cp16(at + c * 16, ks + c * 16);
-                // V: chunks of a 64-byte row exchanged by bit 2 of the key
-                const int sw = D == 128 ? ((c >> 4) & 1) << 5 : 0;
-                kv4::cp16(at + Tile::kOffV + ((c * 16) ^ sw), vs + c * 16);
-              }
-            }
-          }
-          // scales: 2 kNg chunks for each half of K and of V
-          if (lane < 8 * kNg) {
-            const int c = lane % (2 * kNg), h = (lane / (2 * kNg)) & 1, v = lane / (4 * kNg);
-            const uint8_t* src = (v ? p.pool.v_scale : p.pool.k_scale) +
-                                 (h ? row[1] : row[0]) * (2 * kNg) + c * 16;
-            if (h ? on[1] : on[0])
-              kv4::cp16(dst + Tile::kOffKs + v * Tile::kScales + h * (32 * kNg) + c * 16, src);
-          }
+          // lanes: K's scales (two halves), then V's, in the order of the ring
+          if (lane < 8 * kNg) kv4::cp16<Tile::kOffKs, 0>(dst, sc);
+          k_lo += kAttnKeys * (D / 2);
+          k_hi += kAttnKeys * (D / 2);
+          sc += kAttnKeys * (2 * kNg);
         }
-        if (++in.t == in.w.tiles && to_issue > 0 && !in.next_unit(p)) to_issue = 0;
       }
       kv4::cp_commit();
     };
@@ -327,18 +430,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     int stage = 0;
-    long long left = wb - wa;
+    int left = count;
     long long unit_first = wa - cur.t;
     // rows of a block of 16 that this lane reads: keys of rows g, 2 q4, 2 q4 + 1
     const int key_g = g ^ ((g >> 1) & 1);
     const int key_e0 = (2 * q4) ^ (q4 & 1), key_e1 = (2 * q4 + 1) ^ (q4 & 1);
-    const int v_sw = D == 128 ? (((g >> 1) ^ ((q4 >> 1) << 1)) << 4) + (g & 1) * 8 : g * 4;
+    const int k_at = key_g * (D / 2) + q4 * (D / 8);
+    const int v_in = D == 128 ? (((g >> 1) ^ ((q4 >> 1) << 1)) << 4) + (g & 1) * 8 : g * 4;
+    const int v_at0 = Tile::kOffV + key_e0 * (D / 2) + v_in;
+    const int v_at1 = Tile::kOffV + key_e1 * (D / 2) + v_in;
+    const int sc_at = Tile::kOffKs + key_g * (2 * kNg);
 
 #pragma unroll 1
     while (left > 0) {
       // ---- a unit: its queries ----
-      const int n = static_cast<int>(min(left, static_cast<long long>(cur.w.tiles - cur.t)));
-      const bool whole = cur.t == 0 && n == cur.w.tiles;
+      const int t0 = cur.t, keys = cur.keys;
+      const int n = min(left, cur.w.tiles - t0);
+      const bool whole = t0 == 0 && n == cur.w.tiles;
       const bool head = !whole && n < left;  // more tiles of this warp follow
       uint32_t qf[NB][kT][4];
       float cs[NB][2];  // scale of a column's scores, log2 units
@@ -387,8 +495,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
       // ---- its running state ----
       float o[kT][2][NB][4];
-      float m[NB][2], mu[NB][2], l[NB][2];
-      float sig = 0x1p-100f, vmul = 0x1p105f;  // V's power of two, 2^5 over it
+      // per column: the reference r of its probabilities 2^(score - r), the score
+      // that moves it, their sum; per unit: the power of two of V's scales
+      float r[NB][2], mv[NB][2], l[NB][2];
+      float sig = 0x1p-60f;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -397,8 +507,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[t][i][nb][c] = 0.f;
-        m[nb][0] = m[nb][1] = -INFINITY;
-        mu[nb][0] = mu[nb][1] = 0.f;
+        mv[nb][0] = mv[nb][1] = -INFINITY;
+        r[nb][0] = r[nb][1] = 0.f;
         l[nb][0] = l[nb][1] = 0.f;
       }
 
@@ -409,16 +519,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         issue(stage == 0 ? kStages - 1 : stage - 1);
         const uint8_t* st = ring + stage * Tile::kBytes;
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        const int key0 = (cur.t + it) * kAttnKeys;
-        if (key0 >= cur.keys) continue;  // nothing of this tile was fetched
+        const int key0 = (t0 + it) * kAttnKeys;
+        if (key0 >= keys) continue;  // nothing of this tile was fetched
 
-        // scores, log2 units
+        // scores, to be scaled by cs
         float s[2][NB][4];
         uint32_t vsc[2][2][(kNg + 1) / 2];  // V's scales of rows g and g + 8
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
           uint32_t k0[kT], k1[kT];
-          const uint8_t* kr = st + (16 * mb + key_g) * (D / 2) + q4 * (D / 8);
+          const uint8_t* kr = st + k_at + 16 * mb * (D / 2);
           if constexpr (D == 128) {
             const uint4 x = *reinterpret_cast<const uint4*>(kr);
             const uint4 y = *reinterpret_cast<const uint4*>(kr + 8 * (D / 2));
@@ -433,9 +543,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           uint32_t ksc[2][(kNg + 1) / 2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int key = 16 * mb + 8 * h + key_g;
-            const uint8_t* kp = st + Tile::kOffKs + key * (2 * kNg);
-            const uint8_t* vp = st + Tile::kOffVs + key * (2 * kNg);
+            const uint8_t* kp = st + sc_at + (16 * mb + 8 * h) * (2 * kNg);
+            const uint8_t* vp = kp + Tile::kScales;
             if constexpr (kNg == 4) {
               const uint2 x = *reinterpret_cast<const uint2*>(kp), y = *reinterpret_cast<const uint2*>(vp);
               ksc[h][0] = x.x, ksc[h][1] = x.y;
@@ -449,44 +558,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[mb][nb][c] = 0.f;
-#pragma unroll
           for (int i = 0; i < kNg; ++i) {
             float acc[NB][4];
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[nb][c] = 0.f;
-#pragma unroll
             for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
-              const uint32_t x = k0[t], y = k1[t];
-              const uint32_t xh = x >> 8, yh = y >> 8;
+              const uint32_t x = k0[t], y = k1[t], xh = x >> 8, yh = y >> 8;
               const uint32_t ev[4] = {kv4::code_low(x), kv4::code_low(y), kv4::code_low(xh),
                                       kv4::code_low(yh)};
               const uint32_t od[4] = {kv4::code_high(x), kv4::code_high(y), kv4::code_high(xh),
                                       kv4::code_high(yh)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                dec::mma_f16(acc[nb], ev, qf[nb][t][0], qf[nb][t][1]);
+                if (t == i * kTg)
+                  kv4::mma_f16_first(acc[nb], ev, qf[nb][t][0], qf[nb][t][1]);
+                else
+                  dec::mma_f16(acc[nb], ev, qf[nb][t][0], qf[nb][t][1]);
                 dec::mma_f16(acc[nb], od, qf[nb][t][2], qf[nb][t][3]);
               }
             }
-            const float a0 = kv4::unpack1<BF16>((i & 1) ? ksc[0][i / 2] >> 16 : ksc[0][i / 2] & 0xffffu);
-            const float a1 = kv4::unpack1<BF16>((i & 1) ? ksc[1][i / 2] >> 16 : ksc[1][i / 2] & 0xffffu);
+            const float2 f0 = kv4::unpack2<BF16>(ksc[0][i / 2]), f1 = kv4::unpack2<BF16>(ksc[1][i / 2]);
+            const float a0 = (i & 1) ? f0.y : f0.x, a1 = (i & 1) ? f1.y : f1.x;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                s[mb][nb][j] = fmaf(acc[nb][j], a0, s[mb][nb][j]);
-                s[mb][nb][2 + j] = fmaf(acc[nb][2 + j], a1, s[mb][nb][2 + j]);
+                s[mb][nb][j] = i == 0 ? acc[nb][j] * a0 : fmaf(acc[nb][j], a0, s[mb][nb][j]);
+                s[mb][nb][2 + j] =
+                    i == 0 ? acc[nb][2 + j] * a1 : fmaf(acc[nb][2 + j], a1, s[mb][nb][2 + j]);
               }
           }
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) s[mb][nb][c] *= cs[nb][c & 1];
         }
         if (key0 + kAttnKeys > min_lim) {
           // keys that a column does not see; rows past the cache hold whatever
@@ -501,7 +601,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
                   if (key >= lim[nb][j]) s[mb][nb][2 * h + j] = -INFINITY;
-              if (key >= cur.keys) {
+              if (key >= keys) {
 #pragma unroll
                 for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = 0u;
               }
@@ -509,42 +609,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
 
         // running maximum, and the power of two of V's scales
-        float mx[NB][2], vmax = 0.f;
+        float mx[NB][2];
         bool moved = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            mx[nb][j] = fmaxf(fmaxf(s[0][nb][j], s[0][nb][2 + j]), fmaxf(s[1][nb][j], s[1][nb][2 + j]));
-            moved |= mx[nb][j] > m[nb][j] + 8.0f;
+            mx[nb][j] = cs[nb][j] * fmaxf(fmaxf(s[0][nb][j], s[0][nb][2 + j]),
+                                          fmaxf(s[1][nb][j], s[1][nb][2 + j]));
+            moved |= mx[nb][j] > mv[nb][j];
           }
+        uint32_t vm = vsc[0][0][0];
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < kNg; ++i)
-              vmax = fmaxf(vmax, kv4::unpack1<BF16>((i & 1) ? vsc[mb][h][i / 2] >> 16
-                                                            : vsc[mb][h][i / 2] & 0xffffu));
+        for (int x = 1; x < 4 * ((kNg + 1) / 2); ++x)
+          vm = kv4::max2<BF16>(vm, vsc[x & 1][(x >> 1) & 1][x >> 2]);
+        const float2 vm2 = kv4::unpack2<BF16>(vm);  // (one scale per row: the upper half is zero)
+        float vmax = fmaxf(vm2.x, vm2.y);
         moved |= vmax >= 2.0f * sig;
         if (__any_sync(0xffffffffu, moved)) {
           vmax = kv4::max_over_rows(vmax);
           const uint32_t ve = min(__float_as_uint(vmax) >> 23, 220u);
-          const float sig_new = fmaxf(sig, __uint_as_float(ve << 23));
-          const float keep = sig / sig_new;
-          sig = sig_new;
-          vmul = 32.0f / sig;
+          sig = fmaxf(sig, __uint_as_float(ve << 23));
+          const float lg = static_cast<float>(static_cast<int>(__float_as_uint(sig) >> 23) - 127);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const float mn = fmaxf(m[nb][j], kv4::max_over_rows(mx[nb][j]));
-              const float to = mn == -INFINITY ? 0.f : mn;
-              const float al = ptx::ex2(m[nb][j] - to);  // 0 from -infinity
-              m[nb][j] = mn;
-              mu[nb][j] = to;
-              l[nb][j] *= al;
-              const float ao = al * keep;
+              // largest score so far; -infinity while no key was seen
+              const float top_s = fmaxf(mv[nb][j] - 8.0f, kv4::max_over_rows(mx[nb][j]));
+              const float to = top_s == -INFINITY ? r[nb][j] : top_s + lg - 5.0f;
+              const float ao = mv[nb][j] == -INFINITY ? 1.0f : ptx::ex2(r[nb][j] - to);
+              r[nb][j] = to;
+              mv[nb][j] = top_s + 8.0f;
+              l[nb][j] *= ao;
 #pragma unroll
               for (int t = 0; t < kT; ++t)
 #pragma unroll
@@ -561,15 +658,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[mb][nb][c] = ptx::ex2(s[mb][nb][c] - mu[nb][c & 1]);
+            for (int c = 0; c < 4; ++c)
+              s[mb][nb][c] = ptx::ex2(fmaf(s[mb][nb][c], cs[nb][c & 1], -r[nb][c & 1]));
             l[nb][0] += s[mb][nb][0] + s[mb][nb][2];
             l[nb][1] += s[mb][nb][1] + s[mb][nb][3];
           }
           uint32_t v[4][kT / 2];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = 16 * mb + 8 * (e >> 1) + ((e & 1) ? key_e1 : key_e0);
-            const uint8_t* vr = st + Tile::kOffV + key * (D / 2) + v_sw;
+            const uint8_t* vr = st + ((e & 1) ? v_at1 : v_at0) + (16 * mb + 8 * (e >> 1)) * (D / 2);
             if constexpr (D == 128) {
               const uint2 x = *reinterpret_cast<const uint2*>(vr);
               v[e][0] = x.x, v[e][1] = x.y;
@@ -579,10 +676,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < kNg; ++i) {
-            const float f0 =
-                vmul * kv4::unpack1<BF16>((i & 1) ? vsc[mb][0][i / 2] >> 16 : vsc[mb][0][i / 2] & 0xffffu);
-            const float f1 =
-                vmul * kv4::unpack1<BF16>((i & 1) ? vsc[mb][1][i / 2] >> 16 : vsc[mb][1][i / 2] & 0xffffu);
+            const float2 x0 = kv4::unpack2<BF16>(vsc[mb][0][i / 2]), x1 = kv4::unpack2<BF16>(vsc[mb][1][i / 2]);
+            const float f0 = (i & 1) ? x0.y : x0.x, f1 = (i & 1) ? x1.y : x1.x;
             uint32_t pb[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
@@ -616,12 +711,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         // a warp's last tiles leave their state in its ring, which is done with;
         // an earlier unit's (one at most: the warp's first) goes to the workspace
         if (head)
-          part = p.heads + static_cast<size_t>(blockIdx.x * kAttnWarps + warp) * kv4::kPartFloats<D, NB>;
-        else {
-          kv4::cp_wait<0>();
-          __syncwarp();
-          part = reinterpret_cast<float*>(ring);
-        }
+          part = p.heads + static_cast<size_t>(blockIdx.x * kWarps + warp) * kv4::kPartFloats<D, NB>;
+        else
+          part = reinterpret_cast<float*>(ring);  // every copy into it has been waited for
+        __syncwarp();
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -631,7 +724,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           const int col = 8 * nb + 2 * q4 + j;
           int tok, row, hq;
           const bool on = kv4::column<NB>(p, cur.w, cur.kv, cur.block, col, &tok, &row, &hq);
-          const float down = whole ? (lsum == 0.f ? 0.f : 0.03125f * sig / lsum) : 0.03125f * sig;
+          const float down = whole ? (lsum == 0.f ? 0.f : 1.0f / lsum) : 1.0f;
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
             float4 x;
@@ -648,11 +741,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           }
           if (g == 0) {
             if (!whole) {
-              part[kCols * D + col] = m[nb][j];
+              part[kCols * D + col] = lsum == 0.f ? -INFINITY : r[nb][j];
               part[kCols * (D + 1) + col] = lsum;
             } else if (on && p.lse) {
               p.lse[static_cast<size_t>(hq) * p.total_q + row] =
-                  lsum == 0.f ? -INFINITY : (m[nb][j] + __log2f(lsum)) * 0.69314718055994530942f;
+                  lsum == 0.f ? -INFINITY : (r[nb][j] + __log2f(lsum)) * 0.69314718055994530942f;
             }
           }
         }
@@ -660,22 +753,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur.s, cur.kv, cur.block, cur.w.tiles, part};
       left -= n;
       unit_first += cur.w.tiles;
-      if (left > 0 && !cur.next_unit(p)) break;
+      if (left > 0) {
+        kv4::Cursor<NB> c = cur;
+        c.next_unit(p);
+        __syncwarp();
+        if (lane == 0) cur = c;
+        __syncwarp();
+      }
     }
-    kv4::cp_wait<0>();
   }
 
   // ---- the CTA's partial states, unit by unit; what other CTAs share goes on ----
   __syncthreads();
-  float* weight = reinterpret_cast<float*>(attn_smem + kAttnWarps * kStages * Tile::kBytes);
+  float* weight = reinterpret_cast<float*>(attn_smem + kWarps * kStages * Tile::kBytes);
   // Combines the states that `at(i)`, i < n, points to: to the unit's outputs,
   // or (out) to another state.
   const auto combine = [&](const kv4::Part& u, int n, auto at, auto load, float* out) {
     // weights 2^(m_i - M) of each column; [n][kCols]
-    for (int x = tid; x < n * kCols; x += kAttnThreads)
+    for (int x = tid; x < n * kCols; x += kThreads)
       weight[x] = load(at(x / kCols) + kCols * D + x % kCols);
     __syncthreads();
-    for (int col = warp; col < kCols; col += kAttnWarps) {
+    for (int col = warp; col < kCols; col += kWarps) {
       float mm = -INFINITY;
       for (int i = lane; i < n; i += 32) mm = fmaxf(mm, weight[i * kCols + col]);
 #pragma unroll
@@ -695,7 +793,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
     }
     __syncthreads();
-    for (int x = tid; x < kCols * (D / 4); x += kAttnThreads) {
+    for (int x = tid; x < kCols * (D / 4); x += kThreads) {
       const int col = x / (D / 4), ch = 4 * (x % (D / 4));
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -730,7 +828,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     __syncthreads();
   };
-  for (int e = 0; e < 2 * kAttnWarps;) {
+  for (int e = 0; e < 2 * kWarps;) {
     if (!parts[e].at) {
       ++e;
       continue;
@@ -738,7 +836,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // the run of states of one unit (the absent ones between them are skipped)
     const kv4::Part u = parts[e];
     int n = 0, f = e;
-    for (; f < 2 * kAttnWarps; ++f) {
+    for (; f < 2 * kWarps; ++f) {
       if (!parts[f].at) continue;
       if (parts[f].first != u.first) break;
       if (tid == 0) run[n] = parts[f].at;
@@ -780,10 +878,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   }
 }
 
-constexpr int kAttnMaxCtas = 1024;  // TILEMIX_KV4_SYNC_WORDS
-
-Kv4AttnShape kv4_attn_shape(const Kv4Format&, int sms, long long columns) {
-  return {sms < kAttnMaxCtas ? sms : kAttnMaxCtas, kAttnWarps, columns > 8 ? 16 : 8};
+Kv4AttnShape kv4_attn_shape(int sms, long long columns) {
+  const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
+  return columns > 8 ? Kv4AttnShape{ctas, kAttnWarps<2>, 16} : Kv4AttnShape{ctas, kAttnWarps<1>, 8};
 }
 
 struct LaunchAttn {
@@ -796,14 +893,14 @@ struct LaunchAttn {
   }
   template <int D, int GROUP, int NB, bool BF16>
   int run() const {
-    using Tile = AttnTile<D, GROUP>;
-    const int slots = shape.ctas > 2 * kAttnWarps ? shape.ctas : 2 * kAttnWarps;
-    const int smem = kAttnWarps * Tile::kStages * Tile::kBytes + slots * 8 * NB * 4;
+    using Tile = AttnTile<D, GROUP, NB>;
+    constexpr int kWarps = kAttnWarps<NB>;
+    const int smem = kWarps * Tile::kStages * Tile::kBytes + Tile::kWeights;
     const auto kernel = kv4_attn_kernel<D, GROUP, NB, BF16>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return static_cast<int>(e);
-    kernel<<<shape.ctas, kAttnThreads, smem, stream>>>(p);
+    kernel<<<shape.ctas, 32 * kWarps, smem, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }
 };

@@ -66,10 +66,8 @@ struct AttnTile {
   static constexpr int kOffV = kCodes;
   static constexpr int kOffKs = 2 * kCodes;
   static constexpr int kOffVs = 2 * kCodes + kScales;
-  // as many stages as fit beside the merge's weights and 4 KB of the kernel's own,
-  // at most six
-  static constexpr int kWeights = kAttnMaxCtas * 8 * NB * 4;
-  static constexpr int kFit = (223 * 1024 - kWeights) / (kAttnWarps<NB> * kBytes);
+  // as many stages as fit beside 4 KB of the kernel's own, at most six
+  static constexpr int kFit = 223 * 1024 / (kAttnWarps<NB> * kBytes);
   static constexpr int kStages = kFit > 6 ? 6 : kFit;
   static_assert(kStages >= 3, "ring too short");
   static_assert(kStages * kBytes >= 8 * NB * (D + 2) * 4, "a partial state fits a warp's ring");
@@ -156,9 +154,9 @@ struct SeqWork {
 template <int NB>
 __device__ __forceinline__ SeqWork seq_work(const Kv4AttnParams& p, int s) {
   SeqWork w;
-  const long long top = min(static_cast<long long>(p.max_pages) << p.pool.page_shift, 0x7fffff00LL);
-  const int have = __ldg(p.seq_len + s);
-  w.len = static_cast<int>(min(static_cast<long long>(max(have, 0)), top));
+  const int top = static_cast<int>(
+      min(static_cast<long long>(p.max_pages) << p.pool.page_shift, 0x7fffff00LL));
+  w.len = min(max(__ldg(p.seq_len + s), 0), top);
   w.row0 = s;
   w.queries = 1;
   if (p.token_start) {
@@ -171,11 +169,11 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnParams& p, int s) {
   return w;
 }
 __device__ __forceinline__ long long seq_tiles(const Kv4AttnParams& p, const SeqWork& w) {
-  return static_cast<long long>(p.pool.hk) * w.blocks * w.tiles;
+  return static_cast<long long>(p.pool.hk * w.blocks) * w.tiles;
 }
 
 // Column `col` of a unit's block: its row of q and its query head; false for
-// padding (and for rows outside q).
+// padding (and for rows outside q).  total_q * hq < 2^31, so that columns fit.
 template <int NB>
 __device__ __forceinline__ bool column(const Kv4AttnParams& p, const SeqWork& w, int kv, int block,
                                        int col, int* token, int* row, int* head) {
@@ -197,14 +195,17 @@ struct Cursor {
   __device__ __forceinline__ void enter_unit(const Kv4AttnParams& p) {
     kv = u / w.blocks;
     block = u - kv * w.blocks;
-    // total_q * hq < 2^31, so columns fit an unsigned int
     const int last = min(static_cast<int>((block * (8u * NB) + 8u * NB - 1) / p.group_q), w.queries - 1);
     keys = max(0, w.len - w.queries + last + 1);
   }
   __device__ __forceinline__ void start(const Kv4AttnParams& p, int seq, long long off) {
     s = seq;
     w = seq_work<NB>(p, s);
-    u = static_cast<int>(off / w.tiles);
+    w.blocks = max(w.blocks, 1);
+    if (off < 0x7fffffffLL)
+      u = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(w.tiles));
+    else
+      u = static_cast<int>(off / w.tiles);
     t = static_cast<int>(off - static_cast<long long>(u) * w.tiles);
     enter_unit(p);
   }
@@ -223,8 +224,23 @@ struct Cursor {
   }
 };
 
-// A partial state (maximum, sum and unnormalised output of every column of a
-// unit): [columns][D] outputs, then [columns] maxima, then [columns] sums.
+// How the list of all tiles is cut: CTA c has tiles [begin(c), begin(c + 1)).
+struct Cut {
+  long long total, each;  // all tiles; total / ctas
+  int ctas, rest;         // total % ctas
+  __device__ __forceinline__ long long begin(int c) const {  // floor(c * total / ctas)
+    return each * c + static_cast<unsigned>(c * rest) / static_cast<unsigned>(ctas);
+  }
+  // The CTA whose tiles hold tile x.
+  __device__ __forceinline__ int holder(long long x) const {
+    int c = static_cast<int>(min(x / each, static_cast<long long>(ctas - 1)));
+    while (begin(c) > x) --c;
+    return c;
+  }
+};
+
+// A partial state (reference, sum and unnormalised output of every column of a
+// unit): [columns][D] outputs, then [columns] references, then [columns] sums.
 template <int D, int NB>
 constexpr int kPartFloats = 8 * NB * (D + 2);
 
@@ -233,6 +249,46 @@ struct Part {
   int s, kv, block, tiles;
   float* at;        // nullptr: none
 };
+
+// One column's four channels from n states: at(i) is state i.  Sums in order.
+template <int D, int NB, class At, class Load>
+__device__ __forceinline__ float4 combine(int n, int col, int ch, At at, Load load, float* ref,
+                                          float* sum) {
+  constexpr int kCols = 8 * NB;
+  float top = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) top = fmaxf(top, load(at(i) + kCols * D + col));
+  const float to = top == -INFINITY ? 0.f : top;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float w = ptx::ex2(load(at(i) + kCols * D + col) - to);
+    const float4 y = load(reinterpret_cast<const float4*>(at(i) + col * D + ch));
+    l = fmaf(w, load(at(i) + kCols * (D + 1) + col), l);
+    acc.x = fmaf(w, y.x, acc.x);
+    acc.y = fmaf(w, y.y, acc.y);
+    acc.z = fmaf(w, y.z, acc.z);
+    acc.w = fmaf(w, y.w, acc.w);
+  }
+  *ref = top;
+  *sum = l;
+  return acc;
+}
+
+// Four channels of a finished column to O, and its LSE.
+template <int D, int NB, bool BF16>
+__device__ __forceinline__ void store_column(const Kv4AttnParams& p, const SeqWork& w, int kv, int block,
+                                             int col, int ch, const float4& acc, float ref, float sum) {
+  int tok, row, hq;
+  if (!column<NB>(p, w, kv, block, col, &tok, &row, &hq)) return;
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
+      make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
+  if (ch == 0 && p.lse)
+    p.lse[static_cast<size_t>(hq) * p.total_q + row] =
+        sum == 0.f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
+}
 
 }  // namespace kv4
 
@@ -244,83 +300,83 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   constexpr int kNg = Tile::kNg, kT = Tile::kT, kStages = Tile::kStages;
   constexpr int kCols = 8 * NB;
   constexpr int kTg = kT / kNg;  // chunks per scale group
+  static_assert((kWarps & (kWarps - 1)) == 0 && 2 * kWarps <= 32, "runs are found with one ballot");
   extern __shared__ __align__(128) uint8_t attn_smem[];
-  __shared__ long long warp_tiles[kWarps];
-  __shared__ int warp_units[kWarps];
-  __shared__ int start_seq[kWarps];
-  __shared__ long long start_off[kWarps];
   __shared__ kv4::Cursor<NB> cursors[2 * kWarps];
   __shared__ kv4::Part parts[2 * kWarps];
-  __shared__ float* run[2 * kWarps];
-  __shared__ float top[kCols], sum[kCols];
-  __shared__ int merge_last;
+  __shared__ const float* state[2 * kWarps];  // the partial states there are, in order
+  __shared__ int state_of[2 * kWarps];        // ... each one's place in parts
+  __shared__ int run_begin[2 * kWarps + 1], run_count;
+  __shared__ kv4::Cut cut_s;     // for the end: kept out of the registers meanwhile
+  __shared__ long long range_s[2];  // a and b, likewise
+  __shared__ int holders[2][2];  // first and last CTA of a shared unit
+  __shared__ int last_here[2];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
 
-  // ---- the schedule: this CTA's tiles [a, b), this warp's [wa, wb) ----
-  const int per = (p.nseq + kThreads - 1) / kThreads;
-  const int s0 = min(p.nseq, tid * per), s1 = min(p.nseq, s0 + per);
-  long long mine = 0;
-  int units = 0;
-  for (int s = s0; s < s1; ++s) {
-    const kv4::SeqWork w = kv4::seq_work<NB>(p, s);
-    mine += kv4::seq_tiles(p, w);
-    units = min(units + min(p.pool.hk * w.blocks, 0xffff), 0xffff);  // all that matters: fewer than CTAs?
-  }
-  long long inc = mine;
+  // ---- the schedule, by every warp for itself: this warp's tiles [wa, wb) ----
+  long long wa, wb;
+  int seq;
+  long long off;
+  {
+    kv4::Cut cut;
+    const int per = (p.nseq + 31) / 32;
+    const int s0 = min(p.nseq, lane * per), s1 = min(p.nseq, s0 + per);
+    long long mine = 0;
+    int units = 0;
+#pragma unroll 4
+    for (int s = s0; s < s1; ++s) {
+      const kv4::SeqWork w = kv4::seq_work<NB>(p, s);
+      mine += kv4::seq_tiles(p, w);
+      units = min(units + p.pool.hk * w.blocks, 1 << 20);  // all that matters: fewer than CTAs?
+    }
+    long long upto = mine;
 #pragma unroll
-  for (int by = 1; by < 32; by <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, inc, by);
-    if (lane >= by) inc += up;
-  }
-  units = __reduce_add_sync(0xffffffffu, units);
-  if (lane == 31) {
-    warp_tiles[warp] = inc;
-    warp_units[warp] = units;
-  }
-  if (tid < 2 * kWarps) parts[tid].at = nullptr;
-  __syncthreads();
-  long long base = inc - mine, total = 0;
-  units = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) base += warp_tiles[w];
-    total += warp_tiles[w];
-    units += warp_units[w];
-  }
-  // CTAs that take part.  With fewer units than CTAs each unit gets the same
-  // number of them (units of one length are then cut at their own ends, and
-  // none shares a CTA); otherwise the ranges go where they fall.
-  int ctas = gridDim.x;
-  if (units < ctas) {
-    const long long each = total / (static_cast<long long>(max(units, 1)) * kAttnMinTiles);
-    ctas = units * static_cast<int>(max(1LL, min(each, static_cast<long long>(ctas / max(units, 1)))));
-  }
-  if (static_cast<int>(blockIdx.x) >= ctas) return;
-  const auto cta_begin = [&](int c) {
-    return static_cast<long long>(static_cast<unsigned long long>(c) * total /
-                                  static_cast<unsigned>(ctas));
-  };
-  const long long a = cta_begin(blockIdx.x), b = cta_begin(blockIdx.x + 1);
-  const auto warp_begin = [&](int w) { return a + (b - a) * w / kWarps; };
-#pragma unroll 1
-  for (int w = 0; w < kWarps; ++w) {
-    const long long x = warp_begin(w);
-    if (x >= base && x < base + mine) {
-      long long off = x - base;
-      int s = s0;
-      for (;; ++s) {
-        const long long n = kv4::seq_tiles(p, kv4::seq_work<NB>(p, s));
-        if (off < n || s + 1 >= s1) break;
-        off -= n;
-      }
-      start_seq[w] = s;
-      start_off[w] = off;
+    for (int by = 1; by < 32; by <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, upto, by);
+      if (lane >= by) upto += up;
+    }
+    units = __reduce_add_sync(0xffffffffu, units);
+    cut.total = __shfl_sync(0xffffffffu, upto, 31);
+    // CTAs that take part.  With fewer units than CTAs each unit gets the same
+    // number of them (units of one length are then cut at their own ends, and
+    // none shares a CTA); otherwise the ranges go where they fall.
+    cut.ctas = gridDim.x;
+    if (units < cut.ctas) {
+      const int some = static_cast<int>(min(cut.total, 1LL << 30));
+      units = max(units, 1);
+      cut.ctas = units * max(1, min(some / (units * kAttnMinTiles), cut.ctas / units));
+    }
+    if (static_cast<int>(blockIdx.x) >= cut.ctas || cut.total == 0) return;
+    if (cut.total <= 0x7fffffffLL) {
+      cut.each = static_cast<unsigned>(cut.total) / static_cast<unsigned>(cut.ctas);
+    } else {
+      cut.each = cut.total / cut.ctas;
+    }
+    cut.rest = static_cast<int>(cut.total - cut.each * cut.ctas);
+    const long long a = cut.begin(blockIdx.x), b = cut.begin(blockIdx.x + 1);
+    wa = a + (b - a) * warp / kWarps;
+    wb = a + (b - a) * (warp + 1) / kWarps;
+    if (tid == 0) {
+      cut_s = cut;
+      range_s[0] = a;
+      range_s[1] = b;
+    }
+    // the sequence that holds tile wa: the lane's share, then one by one
+    const uint32_t from = __ballot_sync(0xffffffffu, upto - mine <= wa);
+    const int at = 31 - __clz(from);
+    seq = min(at * per, p.nseq - 1);
+    off = wa - __shfl_sync(0xffffffffu, upto - mine, at);
+    for (int i = 1; i < per; ++i) {
+      const long long n = kv4::seq_tiles(p, kv4::seq_work<NB>(p, seq));
+      if (off < n || seq + 1 >= p.nseq) break;
+      off -= n;
+      ++seq;
     }
   }
-  __syncthreads();
-  const long long wa = warp_begin(warp), wb = warp_begin(warp + 1);
+  if (lane < 2) parts[2 * warp + lane].at = nullptr;
+  __syncwarp();
 
   // ---- this warp's tiles ----
   if (wa < wb) {
@@ -331,7 +387,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     kv4::Cursor<NB>& cur = cursors[2 * warp + 1];
     {
       kv4::Cursor<NB> c;
-      c.start(p, start_seq[warp], start_off[warp]);
+      c.start(p, seq, off);
       if (lane == 0) in = cur = c;
       __syncwarp();
     }
@@ -340,8 +396,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     int issued = 0;
     // Copies of a tile, 16 bytes a lane: each half of K's and V's codes (16 keys,
     // within one page) is D / 64 rounds of the warp, all four parts of the
-    // scales together are one.
-    // V's 16-byte chunks of a 64-byte row are exchanged by bit 2 of the key.
+    // scales together are one.  V's 16-byte chunks of a 64-byte row are exchanged by
+    // bit 2 of the key.
     const uint32_t dst0 = ptx::smem_addr(ring) + lane * 16;
     const uint32_t dstv0 = ptx::smem_addr(ring) + Tile::kOffV +
                            (D == 128 ? (lane * 16) ^ ((lane & 16) << 1) : lane * 16);
@@ -708,49 +764,37 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // ---- the unit's end: to the outputs, or a partial state ----
       float* part = nullptr;
       if (!whole) {
-        // a warp's last tiles leave their state in its ring, which is done with;
-        // an earlier unit's (one at most: the warp's first) goes to the workspace
-        if (head)
-          part = p.heads + static_cast<size_t>(blockIdx.x * kWarps + warp) * kv4::kPartFloats<D, NB>;
-        else
-          part = reinterpret_cast<float*>(ring);  // every copy into it has been waited for
-        __syncwarp();
+        // a warp's last tiles leave their state in its ring, which is done with
+        // (every copy into it was waited for); an earlier unit's (one at most: the
+        // warp's first) goes to the workspace
+        part = head ? p.heads + static_cast<size_t>(blockIdx.x * kWarps + warp) * kv4::kPartFloats<D, NB>
+                    : reinterpret_cast<float*>(ring);
+        if (lane == 0)
+          parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur.s, cur.kv, cur.block, cur.w.tiles, part};
       }
+      __syncwarp();
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const float lsum = kv4::sum_over_rows(l[nb][j]);
+          const float ref = lsum == 0.f ? -INFINITY : r[nb][j];
           const int col = 8 * nb + 2 * q4 + j;
-          int tok, row, hq;
-          const bool on = kv4::column<NB>(p, cur.w, cur.kv, cur.block, col, &tok, &row, &hq);
-          const float down = whole ? (lsum == 0.f ? 0.f : 1.0f / lsum) : 1.0f;
 #pragma unroll
           for (int t = 0; t < kT; ++t) {
-            float4 x;
-            x.x = o[t][0][nb][j] * down;
-            x.y = o[t][1][nb][j] * down;
-            x.z = o[t][0][nb][2 + j] * down;
-            x.w = o[t][1][nb][2 + j] * down;
+            const float4 x = make_float4(o[t][0][nb][j], o[t][1][nb][j], o[t][0][nb][2 + j],
+                                         o[t][1][nb][2 + j]);
             const int ch = 32 * t + 4 * g;
             if (!whole)
               *reinterpret_cast<float4*>(part + col * D + ch) = x;
-            else if (on)
-              *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
-                  make_uint2(kv4::pack2<BF16>(x.x, x.y), kv4::pack2<BF16>(x.z, x.w));
+            else
+              kv4::store_column<D, NB, BF16>(p, cur.w, cur.kv, cur.block, col, ch, x, ref, lsum);
           }
-          if (g == 0) {
-            if (!whole) {
-              part[kCols * D + col] = lsum == 0.f ? -INFINITY : r[nb][j];
-              part[kCols * (D + 1) + col] = lsum;
-            } else if (on && p.lse) {
-              p.lse[static_cast<size_t>(hq) * p.total_q + row] =
-                  lsum == 0.f ? -INFINITY : (r[nb][j] + __log2f(lsum)) * 0.69314718055994530942f;
-            }
+          if (!whole && g == 0) {
+            part[kCols * D + col] = ref;
+            part[kCols * (D + 1) + col] = lsum;
           }
         }
-      if (!whole && lane == 0)
-        parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur.s, cur.kv, cur.block, cur.w.tiles, part};
       left -= n;
       unit_first += cur.w.tiles;
       if (left > 0) {
@@ -763,118 +807,89 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     }
   }
 
-  // ---- the CTA's partial states, unit by unit; what other CTAs share goes on ----
+  // ---- the CTA's partial states; what other CTAs share goes on ----
+  // States lie in the order of the tiles, so those of one unit are neighbours:
+  // a run.  Every run at once, a thread to a column's four channels; each unit
+  // that lies within the CTA is finished, the first and the last may be shared.
   __syncthreads();
-  float* weight = reinterpret_cast<float*>(attn_smem + kWarps * kStages * Tile::kBytes);
-  // Combines the states that `at(i)`, i < n, points to: to the unit's outputs,
-  // or (out) to another state.
-  const auto combine = [&](const kv4::Part& u, int n, auto at, auto load, float* out) {
-    // weights 2^(m_i - M) of each column; [n][kCols]
-    for (int x = tid; x < n * kCols; x += kThreads)
-      weight[x] = load(at(x / kCols) + kCols * D + x % kCols);
-    __syncthreads();
-    for (int col = warp; col < kCols; col += kWarps) {
-      float mm = -INFINITY;
-      for (int i = lane; i < n; i += 32) mm = fmaxf(mm, weight[i * kCols + col]);
-#pragma unroll
-      for (int by = 16; by > 0; by >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, by));
-      const float to = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      for (int i = lane; i < n; i += 32) {
-        const float w = ptx::ex2(weight[i * kCols + col] - to);
-        weight[i * kCols + col] = w;
-        ll += w * load(at(i) + kCols * (D + 1) + col);
-      }
-#pragma unroll
-      for (int by = 16; by > 0; by >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, by);
-      if (lane == 0) {
-        top[col] = mm;
-        sum[col] = ll;
-      }
+  constexpr int kItems = kCols * (D / 4), kPart = kv4::kPartFloats<D, NB>;
+  if (warp == 0) {
+    const bool present = lane < 2 * kWarps && parts[lane].at != nullptr;
+    const uint32_t here = __ballot_sync(0xffffffffu, present);
+    const uint32_t before = here & ((1u << lane) - 1u);
+    const bool begins =
+        present && (before == 0 || parts[31 - __clz(before)].first != parts[lane].first);
+    const uint32_t starts = __ballot_sync(0xffffffffu, begins);
+    if (present) {
+      state[__popc(before)] = parts[lane].at;
+      state_of[__popc(before)] = lane;
     }
-    __syncthreads();
-    for (int x = tid; x < kCols * (D / 4); x += kThreads) {
-      const int col = x / (D / 4), ch = 4 * (x % (D / 4));
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float w = weight[i * kCols + col];
-        const float4 y = load(reinterpret_cast<const float4*>(at(i) + col * D + ch));
-        acc.x = fmaf(w, y.x, acc.x);
-        acc.y = fmaf(w, y.y, acc.y);
-        acc.z = fmaf(w, y.z, acc.z);
-        acc.w = fmaf(w, y.w, acc.w);
-      }
-      const float mm = top[col], ll = sum[col];
-      if (out) {
-        *reinterpret_cast<float4*>(out + col * D + ch) = acc;
-        if (ch == 0) {
-          out[kCols * D + col] = mm;
-          out[kCols * (D + 1) + col] = ll;
-        }
-      } else {
-        const kv4::SeqWork sw = kv4::seq_work<NB>(p, u.s);
-        int tok, row, hq;
-        if (kv4::column<NB>(p, sw, u.kv, u.block, col, &tok, &row, &hq)) {
-          const float inv = ll == 0.f ? 0.f : 1.0f / ll;
-          *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
-              make_uint2(kv4::pack2<BF16>(acc.x * inv, acc.y * inv),
-                         kv4::pack2<BF16>(acc.z * inv, acc.w * inv));
-          if (ch == 0 && p.lse)
-            p.lse[static_cast<size_t>(hq) * p.total_q + row] =
-                ll == 0.f ? -INFINITY : (mm + __log2f(ll)) * 0.69314718055994530942f;
-        }
+    if (begins) run_begin[__popc(starts & ((1u << lane) - 1u))] = __popc(before);
+    if (lane == 0) {
+      run_count = __popc(starts);
+      run_begin[__popc(starts)] = __popc(here);
+    }
+  }
+  __syncthreads();
+  const int runs = run_count;
+  const long long a = range_s[0], b = range_s[1];
+  const auto shared_unit = [&](const kv4::Part& u) { return u.first < a || u.first + u.tiles > b; };
+  for (int x = tid; x < runs * kItems; x += kThreads) {
+    const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
+    const float* const* states = state + run_begin[i];
+    const kv4::Part u = parts[state_of[run_begin[i]]];
+    float ref, sum;
+    const float4 acc = kv4::combine<D, NB>(
+        run_begin[i + 1] - run_begin[i], col, ch, [&](int k) { return states[k]; },
+        [](const auto* y) { return *y; },  // shared memory, or this CTA's own
+        &ref, &sum);
+    if (!shared_unit(u)) {
+      kv4::store_column<D, NB, BF16>(p, kv4::seq_work<NB>(p, u.s), u.kv, u.block, col, ch, acc, ref, sum);
+    } else {
+      // to this CTA's first place (the unit began before its tiles) or second
+      float* out = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart;
+      *reinterpret_cast<float4*>(out + col * D + ch) = acc;
+      if (ch == 0) {
+        out[kCols * D + col] = ref;
+        out[kCols * (D + 1) + col] = sum;
       }
     }
-    __syncthreads();
-  };
-  for (int e = 0; e < 2 * kWarps;) {
-    if (!parts[e].at) {
-      ++e;
-      continue;
-    }
-    // the run of states of one unit (the absent ones between them are skipped)
-    const kv4::Part u = parts[e];
-    int n = 0, f = e;
-    for (; f < 2 * kWarps; ++f) {
-      if (!parts[f].at) continue;
-      if (parts[f].first != u.first) break;
-      if (tid == 0) run[n] = parts[f].at;
-      ++n;
-    }
-    e = f;
-    __syncthreads();
-    const auto of_run = [&](int i) { return static_cast<const float*>(run[i]); };
-    const auto plain = [](const auto* x) { return *x; };  // shared memory, or this CTA's own
-    if (u.first >= a && u.first + u.tiles <= b) {
-      combine(u, n, of_run, plain, nullptr);
-      continue;
-    }
-    // The unit is shared with other CTAs: this one's state goes to its first
-    // place (the unit began before this CTA's tiles) or its second, and the
-    // last of the unit's CTAs to arrive combines them all, in order.
-    constexpr int kPart = kv4::kPartFloats<D, NB>;
-    combine(u, n, of_run, plain,
-            p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart);
-    const auto cta_of = [&](long long x) {  // the CTA whose tiles hold tile x
-      return static_cast<int>(((x + 1) * ctas - 1) / total);
-    };
-    const int c0 = cta_of(u.first), c1 = cta_of(u.first + u.tiles - 1);
-    if (tid == 0) {
+  }
+  // The first and the last unit: the last of the CTAs that share one to arrive
+  // combines all of their states, in order.
+  if (runs == 0) return;
+  const kv4::Part ends[2] = {parts[state_of[0]], parts[state_of[run_begin[runs - 1]]]};
+  const bool shares[2] = {shared_unit(ends[0]), runs > 1 && shared_unit(ends[1])};
+  if (!shares[0] && !shares[1]) return;
+  __syncthreads();
+  if (lane == 0 && warp < 2) {
+    last_here[warp] = 0;
+    if (warp == 0 ? shares[0] : shares[1]) {
+      const kv4::Part u = warp == 0 ? ends[0] : ends[1];
+      const int c0 = cut_s.holder(u.first), c1 = cut_s.holder(u.first + u.tiles - 1);
+      holders[warp][0] = c0;
+      holders[warp][1] = c1;
       __threadfence();
       // wraps to zero with the last arrival, so the array is zero again
-      merge_last = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+      last_here[warp] = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
       __threadfence();
     }
-    __syncthreads();
-    if (merge_last)
-      combine(u, c1 - c0 + 1,
-              [&](int i) {
-                return static_cast<const float*>(
-                    p.parts + (2 * static_cast<size_t>(c0 + i) + (i == 0 ? 1 : 0)) * kPart);
-              },
-              [](const auto* x) { return __ldcg(x); }, nullptr);
-    __syncthreads();
+  }
+  __syncthreads();
+  for (int x = tid; x < 2 * kItems; x += kThreads) {
+    const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
+    if (!last_here[i]) continue;
+    const kv4::Part& u = i == 0 ? ends[0] : ends[1];
+    const int c0 = holders[i][0];
+    float ref, sum;
+    const float4 acc = kv4::combine<D, NB>(
+        holders[i][1] - c0 + 1, col, ch,
+        [&](int k) {
+          return static_cast<const float*>(p.parts +
+                                           (2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0)) * kPart);
+        },
+        [](const auto* y) { return __ldcg(y); }, &ref, &sum);
+    kv4::store_column<D, NB, BF16>(p, kv4::seq_work<NB>(p, u.s), u.kv, u.block, col, ch, acc, ref, sum);
   }
 }
 
@@ -895,7 +910,7 @@ struct LaunchAttn {
   int run() const {
     using Tile = AttnTile<D, GROUP, NB>;
     constexpr int kWarps = kAttnWarps<NB>;
-    const int smem = kWarps * Tile::kStages * Tile::kBytes + Tile::kWeights;
+    const int smem = kWarps * Tile::kStages * Tile::kBytes;
     const auto kernel = kv4_attn_kernel<D, GROUP, NB, BF16>;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

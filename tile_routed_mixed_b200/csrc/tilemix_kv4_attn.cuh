@@ -185,44 +185,31 @@ __device__ __forceinline__ bool column(const Kv4AttnParams& p, const SeqWork& w,
   return *token < w.queries && *row >= 0 && *row < p.total_q;
 }
 
-// A place in the list of all tiles: tile t of unit u of sequence s.
-template <int NB>
-struct Cursor {
-  int s, u, t;
+// A unit as a warp meets it.
+struct Unit {
   SeqWork w;
-  int kv, block;
+  int s, kv, block;
   int keys;  // keys that some column of the unit may see
-  __device__ __forceinline__ void enter_unit(const Kv4AttnParams& p) {
-    kv = u / w.blocks;
-    block = u - kv * w.blocks;
-    const int last = min(static_cast<int>((block * (8u * NB) + 8u * NB - 1) / p.group_q), w.queries - 1);
-    keys = max(0, w.len - w.queries + last + 1);
-  }
-  __device__ __forceinline__ void start(const Kv4AttnParams& p, int seq, long long off) {
-    s = seq;
-    w = seq_work<NB>(p, s);
-    w.blocks = max(w.blocks, 1);
-    if (off < 0x7fffffffLL)
-      u = static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(w.tiles));
-    else
-      u = static_cast<int>(off / w.tiles);
-    t = static_cast<int>(off - static_cast<long long>(u) * w.tiles);
-    enter_unit(p);
-  }
-  // To the first tile of the next unit; there is one.
-  __device__ __forceinline__ void next_unit(const Kv4AttnParams& p) {
-    t = 0;
-    if (++u == p.pool.hk * w.blocks) {
-      u = 0;
-      do {
-        s = min(s + 1, p.nseq - 1);
-        w = seq_work<NB>(p, s);
-      } while (w.blocks == 0 && s + 1 < p.nseq);
-      w.blocks = max(w.blocks, 1);
-    }
-    enter_unit(p);
-  }
 };
+// The unit after x, in the order sequence, KV head, block; there is one.
+template <int NB>
+__device__ __forceinline__ Unit unit_after(const Kv4AttnParams& p, Unit x) {
+  int u = x.kv * x.w.blocks + x.block + 1;
+  if (u == p.pool.hk * x.w.blocks) {
+    u = 0;
+    do {  // a sequence without queries has no unit
+      x.s = min(x.s + 1, p.nseq - 1);
+      x.w = seq_work<NB>(p, x.s);
+    } while (x.w.blocks == 0 && x.s + 1 < p.nseq);
+    x.w.blocks = max(x.w.blocks, 1);
+  }
+  x.kv = u / x.w.blocks;
+  x.block = u - x.kv * x.w.blocks;
+  const int last =
+      min(static_cast<int>((x.block * (8u * NB) + 8u * NB - 1) / p.group_q), x.w.queries - 1);
+  x.keys = max(0, x.w.len - x.w.queries + last + 1);
+  return x;
+}
 
 // How the list of all tiles is cut: CTA c has tiles [begin(c), begin(c + 1)).
 struct Cut {
@@ -246,30 +233,44 @@ constexpr int kPartFloats = 8 * NB * (D + 2);
 
 struct Part {
   long long first;  // the unit's first tile in the list of all tiles
-  int s, kv, block, tiles;
+  Unit unit;
   float* at;        // nullptr: none
 };
 
-// One column's four channels from n states: at(i) is state i.  Sums in order.
-template <int D, int NB, class At, class Load>
-__device__ __forceinline__ float4 combine(int n, int col, int ch, At at, Load load, float* ref,
-                                          float* sum) {
-  constexpr int kCols = 8 * NB;
+// One column's four channels from n states: at(i) is state i.  The D / 4 lanes
+// of a column take the states' weights together, one each, and then add up the
+// states in order.
+template <int D, int NB, class At>
+__device__ __forceinline__ float4 combine(int n, int col, int ch, At at, float* ref, float* sum) {
+  constexpr int kCols = 8 * NB, kLanes = D / 4;
+  const int mine = ch / 4, first = (threadIdx.x & 31) - mine;  // of the column's lanes
+  const unsigned who = kLanes == 32 ? 0xffffffffu : 0xffffu << first;
   float top = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) top = fmaxf(top, load(at(i) + kCols * D + col));
+#pragma unroll 1
+  for (int i = mine; i < n; i += kLanes) top = fmaxf(top, at(i)[kCols * D + col]);
+#pragma unroll 1
+  for (int by = kLanes / 2; by > 0; by >>= 1) top = fmaxf(top, __shfl_xor_sync(who, top, by));
   const float to = top == -INFINITY ? 0.f : top;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float l = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float w = ptx::ex2(load(at(i) + kCols * D + col) - to);
-    const float4 y = load(reinterpret_cast<const float4*>(at(i) + col * D + ch));
-    l = fmaf(w, load(at(i) + kCols * (D + 1) + col), l);
-    acc.x = fmaf(w, y.x, acc.x);
-    acc.y = fmaf(w, y.y, acc.y);
-    acc.z = fmaf(w, y.z, acc.z);
-    acc.w = fmaf(w, y.w, acc.w);
+#pragma unroll 1
+  for (int base = 0; base < n; base += kLanes) {
+    const int i = base + mine, m = min(n - base, kLanes);
+    float w = 0.f, li = 0.f;
+    if (i < n) {
+      w = ptx::ex2(at(i)[kCols * D + col] - to);
+      li = at(i)[kCols * (D + 1) + col];
+    }
+#pragma unroll 4
+    for (int k = 0; k < m; ++k) {
+      const float4 y = *reinterpret_cast<const float4*>(at(base + k) + col * D + ch);
+      const float wk = __shfl_sync(who, w, first + k);
+      l = fmaf(wk, __shfl_sync(who, li, first + k), l);
+      acc.x = fmaf(wk, y.x, acc.x);
+      acc.y = fmaf(wk, y.y, acc.y);
+      acc.z = fmaf(wk, y.z, acc.z);
+      acc.w = fmaf(wk, y.w, acc.w);
+    }
   }
   *ref = top;
   *sum = l;
@@ -278,10 +279,10 @@ __device__ __forceinline__ float4 combine(int n, int col, int ch, At at, Load lo
 
 // Four channels of a finished column to O, and its LSE.
 template <int D, int NB, bool BF16>
-__device__ __forceinline__ void store_column(const Kv4AttnParams& p, const SeqWork& w, int kv, int block,
-                                             int col, int ch, const float4& acc, float ref, float sum) {
+__device__ __forceinline__ void store_column(const Kv4AttnParams& p, const Unit& u, int col, int ch,
+                                             const float4& acc, float ref, float sum) {
   int tok, row, hq;
-  if (!column<NB>(p, w, kv, block, col, &tok, &row, &hq)) return;
+  if (!column<NB>(p, u.w, u.kv, u.block, col, &tok, &row, &hq)) return;
   const float inv = sum == 0.f ? 0.f : 1.0f / sum;
   *reinterpret_cast<uint2*>(p.o + ((static_cast<size_t>(row) * p.hq + hq) * D + ch) * 2) =
       make_uint2(pack2<BF16>(acc.x * inv, acc.y * inv), pack2<BF16>(acc.z * inv, acc.w * inv));
@@ -300,9 +301,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   constexpr int kNg = Tile::kNg, kT = Tile::kT, kStages = Tile::kStages;
   constexpr int kCols = 8 * NB;
   constexpr int kTg = kT / kNg;  // chunks per scale group
-  static_assert((kWarps & (kWarps - 1)) == 0 && 2 * kWarps <= 32, "runs are found with one ballot");
+  static_assert(2 * kWarps <= 32, "runs are found with one ballot");
   extern __shared__ __align__(128) uint8_t attn_smem[];
-  __shared__ kv4::Cursor<NB> cursors[2 * kWarps];
+  __shared__ kv4::Unit units_ahead[kWarps][8];  // from the one computed to the one fetched
+  static_assert(kStages < 8, "a tile ahead may be a unit ahead");
   __shared__ kv4::Part parts[2 * kWarps];
   __shared__ const float* state[2 * kWarps];  // the partial states there are, in order
   __shared__ int state_of[2 * kWarps];        // ... each one's place in parts
@@ -318,14 +320,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   // ---- the schedule, by every warp for itself: this warp's tiles [wa, wb) ----
   long long wa, wb;
   int seq;
-  long long off;
+  long long off;  // of tile wa within sequence seq's tiles
+  kv4::SeqWork seq_at;
   {
     kv4::Cut cut;
     const int per = (p.nseq + 31) / 32;
     const int s0 = min(p.nseq, lane * per), s1 = min(p.nseq, s0 + per);
     long long mine = 0;
     int units = 0;
-#pragma unroll 4
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const kv4::SeqWork w = kv4::seq_work<NB>(p, s);
       mine += kv4::seq_tiles(p, w);
@@ -368,12 +371,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     const int at = 31 - __clz(from);
     seq = min(at * per, p.nseq - 1);
     off = wa - __shfl_sync(0xffffffffu, upto - mine, at);
-    for (int i = 1; i < per; ++i) {
-      const long long n = kv4::seq_tiles(p, kv4::seq_work<NB>(p, seq));
-      if (off < n || seq + 1 >= p.nseq) break;
+#pragma unroll 1
+    for (int i = 1;; ++i) {
+      seq_at = kv4::seq_work<NB>(p, seq);
+      const long long n = kv4::seq_tiles(p, seq_at);
+      if (off < n || i >= per || seq + 1 >= p.nseq) break;
       off -= n;
       ++seq;
     }
+    seq_at.blocks = max(seq_at.blocks, 1);
   }
   if (lane < 2) parts[2 * warp + lane].at = nullptr;
   __syncwarp();
@@ -381,16 +387,16 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   // ---- this warp's tiles ----
   if (wa < wb) {
     uint8_t* ring = attn_smem + warp * (kStages * Tile::kBytes);
-    // the next tile to fetch, and the unit being computed: kept in shared memory
-    // but for what a tile needs
-    kv4::Cursor<NB>& in = cursors[2 * warp];
-    kv4::Cursor<NB>& cur = cursors[2 * warp + 1];
-    {
-      kv4::Cursor<NB> c;
-      c.start(p, seq, off);
-      if (lane == 0) in = cur = c;
-      __syncwarp();
-    }
+    kv4::Unit* ahead = units_ahead[warp];
+    // tile wa: in unit u of sequence seq, whose predecessor stands in the list
+    const int u = off <= 0x7fffffffLL
+                      ? static_cast<int>(static_cast<unsigned>(off) / static_cast<unsigned>(seq_at.tiles))
+                      : static_cast<int>(off / seq_at.tiles);
+    const int t_first = static_cast<int>(off - static_cast<long long>(u) * seq_at.tiles);
+    if (lane == 0) ahead[7] = {seq_at, seq, 0, u - 1, 0};
+    __syncwarp();
+    int in_t = 0, in_tiles = 0, in_keys = 0, in_kv = 0, in_units = 0;
+    const int32_t* in_table = nullptr;
     const int page_sh = p.pool.page_shift, page_1 = (1 << page_sh) - 1;
     const int count = static_cast<int>(wb - wa);
     int issued = 0;
@@ -404,9 +410,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     const int64_t v_minus_k = p.pool.v_codes - p.pool.k_codes;
     const int sc_half = (lane / (2 * kNg)) & 1;
     const uint8_t* sc_src = (lane < 4 * kNg ? p.pool.k_scale : p.pool.v_scale) + (lane % (2 * kNg)) * 16;
-    int in_t = in.t, in_keys = in.keys, in_tiles = in.w.tiles, in_kv = in.kv;
-    const int32_t* in_table = p.block_table + static_cast<size_t>(in.s) * p.max_pages;
-    int page_next = in_t * kAttnKeys < in_keys ? __ldg(in_table + ((in_t * kAttnKeys) >> page_sh)) : 0;
+    int page_next = 0;
     // Tiles are fetched in runs: tiles of one page, or (run_reads false) tiles
     // that no column sees, which are passed over.  A run's sources: this lane's
     // 16 bytes of the first and second sixteen keys of K, and of the scales.
@@ -415,22 +419,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     const uint8_t *k_lo = nullptr, *k_hi = nullptr, *sc = nullptr;
     const auto next_run = [&]() {
       if (in_t == in_tiles) {
-        kv4::Cursor<NB> c = in;
-        c.next_unit(p);
+        const kv4::Unit x = kv4::unit_after<NB>(p, ahead[(in_units - 1) & 7]);
+        if (lane == 0) ahead[in_units & 7] = x;
         __syncwarp();
-        if (lane == 0) in = c;
-        __syncwarp();
-        in_t = 0, in_keys = c.keys, in_tiles = c.w.tiles, in_kv = c.kv;
-        in_table = p.block_table + static_cast<size_t>(c.s) * p.max_pages;
-        page_next = in_keys > 0 ? __ldg(in_table) : 0;
+        in_t = in_units == 0 ? t_first : 0;
+        ++in_units;
+        in_keys = x.keys, in_tiles = x.w.tiles, in_kv = x.kv;
+        in_table = p.block_table + static_cast<size_t>(x.s) * p.max_pages;
+        if (in_t * kAttnKeys < in_keys) page_next = __ldg(in_table + ((in_t * kAttnKeys) >> page_sh));
       }
       const int key = in_t * kAttnKeys;
       run_reads = key < in_keys;
       if (!run_reads) {
         run = in_tiles - in_t;
         in_t = in_tiles;
-        return;
-      }
+      } else {
       // a page outside the pool is reported, and page 0 read in its place
       int lo = page_next, hi = page_next;
       if (page_sh == 4) {
@@ -453,6 +456,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       in_t += run;
       const int then = in_t * kAttnKeys;
       if (then < in_keys) page_next = __ldg(in_table + (then >> page_sh));
+      }
     };
 
     // Fetches the next tile into `stage`.
@@ -487,7 +491,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
 
     int stage = 0;
     int left = count;
-    long long unit_first = wa - cur.t;
+    int units_done = 0;
+    long long unit_first = wa - t_first;
     // rows of a block of 16 that this lane reads: keys of rows g, 2 q4, 2 q4 + 1
     const int key_g = g ^ ((g >> 1) & 1);
     const int key_e0 = (2 * q4) ^ (q4 & 1), key_e1 = (2 * q4 + 1) ^ (q4 & 1);
@@ -500,7 +505,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
 #pragma unroll 1
     while (left > 0) {
       // ---- a unit: its queries ----
-      const int t0 = cur.t, keys = cur.keys;
+      const kv4::Unit& cur = ahead[units_done & 7];
+      const int t0 = units_done == 0 ? t_first : 0, keys = cur.keys;
       const int n = min(left, cur.w.tiles - t0);
       const bool whole = t0 == 0 && n == cur.w.tiles;
       const bool head = !whole && n < left;  // more tiles of this warp follow
@@ -770,7 +776,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         part = head ? p.heads + static_cast<size_t>(blockIdx.x * kWarps + warp) * kv4::kPartFloats<D, NB>
                     : reinterpret_cast<float*>(ring);
         if (lane == 0)
-          parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur.s, cur.kv, cur.block, cur.w.tiles, part};
+          parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur, part};
       }
       __syncwarp();
 #pragma unroll
@@ -788,7 +794,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
             if (!whole)
               *reinterpret_cast<float4*>(part + col * D + ch) = x;
             else
-              kv4::store_column<D, NB, BF16>(p, cur.w, cur.kv, cur.block, col, ch, x, ref, lsum);
+              kv4::store_column<D, NB, BF16>(p, cur, col, ch, x, ref, lsum);
           }
           if (!whole && g == 0) {
             part[kCols * D + col] = ref;
@@ -797,13 +803,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         }
       left -= n;
       unit_first += cur.w.tiles;
-      if (left > 0) {
-        kv4::Cursor<NB> c = cur;
-        c.next_unit(p);
-        __syncwarp();
-        if (lane == 0) cur = c;
-        __syncwarp();
-      }
+      ++units_done;
     }
   }
 
@@ -812,7 +812,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   // a run.  Every run at once, a thread to a column's four channels; each unit
   // that lies within the CTA is finished, the first and the last may be shared.
   __syncthreads();
-  constexpr int kItems = kCols * (D / 4), kPart = kv4::kPartFloats<D, NB>;
+  constexpr int kItems = kCols * (D / 4);
+  constexpr size_t kPart = kv4::kPartFloats<D, NB>;
   if (warp == 0) {
     const bool present = lane < 2 * kWarps && parts[lane].at != nullptr;
     const uint32_t here = __ballot_sync(0xffffffffu, present);
@@ -833,63 +834,63 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   __syncthreads();
   const int runs = run_count;
   const long long a = range_s[0], b = range_s[1];
-  const auto shared_unit = [&](const kv4::Part& u) { return u.first < a || u.first + u.tiles > b; };
-  for (int x = tid; x < runs * kItems; x += kThreads) {
-    const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
-    const float* const* states = state + run_begin[i];
-    const kv4::Part u = parts[state_of[run_begin[i]]];
-    float ref, sum;
-    const float4 acc = kv4::combine<D, NB>(
-        run_begin[i + 1] - run_begin[i], col, ch, [&](int k) { return states[k]; },
-        [](const auto* y) { return *y; },  // shared memory, or this CTA's own
-        &ref, &sum);
-    if (!shared_unit(u)) {
-      kv4::store_column<D, NB, BF16>(p, kv4::seq_work<NB>(p, u.s), u.kv, u.block, col, ch, acc, ref, sum);
-    } else {
-      // to this CTA's first place (the unit began before its tiles) or second
-      float* out = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart;
-      *reinterpret_cast<float4*>(out + col * D + ch) = acc;
-      if (ch == 0) {
-        out[kCols * D + col] = ref;
-        out[kCols * (D + 1) + col] = sum;
+  if (runs == 0) return;
+  const auto shared_unit = [&](const kv4::Part& u) {
+    return u.first < a || u.first + u.unit.w.tiles > b;
+  };
+  // First each run; then, of the first and the last unit (0 and 1 below) those
+  // that are shared, if this CTA is the last of theirs to arrive: all of the
+  // unit's CTAs' states, in order.
+  const int ends[2] = {state_of[0], state_of[run_begin[runs - 1]]};
+  bool again = false;
+#pragma unroll 1
+  for (int items = runs * kItems;; items = 2 * kItems) {
+#pragma unroll 1
+    for (int x = tid; x < items; x += kThreads) {
+      const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
+      if (again && !last_here[i]) continue;
+      const kv4::Part& u = parts[again ? (i == 0 ? ends[0] : ends[1]) : state_of[run_begin[i]]];
+      const int c0 = again ? holders[i][0] : 0;
+      const int n = again ? holders[i][1] - c0 + 1 : run_begin[i + 1] - run_begin[i];
+      const float* const* states = state + (again ? 0 : run_begin[i]);
+      const float* cta_states = p.parts + static_cast<size_t>(2 * c0) * kPart;
+      float ref, sum;
+      const float4 acc = kv4::combine<D, NB>(
+          n, col, ch,
+          [&](int k) { return again ? cta_states + (k == 0 ? 1 : 2 * k) * kPart : states[k]; }, &ref, &sum);
+      if (again || !shared_unit(u)) {
+        kv4::store_column<D, NB, BF16>(p, u.unit, col, ch, acc, ref, sum);
+      } else {
+        // to this CTA's first place (the unit began before its tiles) or second
+        float* out = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart;
+        *reinterpret_cast<float4*>(out + col * D + ch) = acc;
+        if (ch == 0) {
+          out[kCols * D + col] = ref;
+          out[kCols * (D + 1) + col] = sum;
+        }
       }
     }
-  }
-  // The first and the last unit: the last of the CTAs that share one to arrive
-  // combines all of their states, in order.
-  if (runs == 0) return;
-  const kv4::Part ends[2] = {parts[state_of[0]], parts[state_of[run_begin[runs - 1]]]};
-  const bool shares[2] = {shared_unit(ends[0]), runs > 1 && shared_unit(ends[1])};
-  if (!shares[0] && !shares[1]) return;
-  __syncthreads();
-  if (lane == 0 && warp < 2) {
-    last_here[warp] = 0;
-    if (warp == 0 ? shares[0] : shares[1]) {
-      const kv4::Part u = warp == 0 ? ends[0] : ends[1];
-      const int c0 = cut_s.holder(u.first), c1 = cut_s.holder(u.first + u.tiles - 1);
-      holders[warp][0] = c0;
-      holders[warp][1] = c1;
-      __threadfence();
-      // wraps to zero with the last arrival, so the array is zero again
-      last_here[warp] = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
-      __threadfence();
+    if (again) return;
+    again = true;
+    const bool shares0 = shared_unit(parts[ends[0]]);
+    const bool shares1 = runs > 1 && shared_unit(parts[ends[1]]);
+    if (!shares0 && !shares1) return;
+    __syncthreads();
+    if (lane == 0 && warp < 2) {
+      int last = 0;
+      if (warp == 0 ? shares0 : shares1) {
+        const kv4::Part& u = parts[warp == 0 ? ends[0] : ends[1]];
+        const int c0 = cut_s.holder(u.first), c1 = cut_s.holder(u.first + u.unit.w.tiles - 1);
+        holders[warp][0] = c0;
+        holders[warp][1] = c1;
+        __threadfence();
+        // wraps to zero with the last arrival, so the array is zero again
+        last = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
+        __threadfence();
+      }
+      last_here[warp] = last;
     }
-  }
-  __syncthreads();
-  for (int x = tid; x < 2 * kItems; x += kThreads) {
-    const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
-    if (!last_here[i]) continue;
-    const kv4::Part& u = i == 0 ? ends[0] : ends[1];
-    const int c0 = holders[i][0];
-    float ref, sum;
-    const float4 acc = kv4::combine<D, NB>(
-        holders[i][1] - c0 + 1, col, ch,
-        [&](int k) {
-          return static_cast<const float*>(p.parts +
-                                           (2 * static_cast<size_t>(c0 + k) + (k == 0 ? 1 : 0)) * kPart);
-        },
-        [](const auto* y) { return __ldcg(y); }, &ref, &sum);
-    kv4::store_column<D, NB, BF16>(p, kv4::seq_work<NB>(p, u.s), u.kv, u.block, col, ch, acc, ref, sum);
+    __syncthreads();
   }
 }
 

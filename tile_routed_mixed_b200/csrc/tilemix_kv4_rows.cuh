@@ -21,6 +21,9 @@
 namespace tilemix {
 
 constexpr int kRowThreads = 256;
+// Chunks from which a thread takes four (of fewer, one each spreads them over
+// more SMs): two full waves of one each.
+constexpr long long kRowsWide = 148LL * 2048 * 2;
 
 namespace kv4 {
 
@@ -101,70 +104,83 @@ __device__ __forceinline__ int k_place(int w) {
 
 }  // namespace kv4
 
-// One chunk of 8 channels per thread; blockIdx.y picks K or V.
-template <int D, int GROUP, bool BF16>
+// U chunks of 8 channels per thread, all loaded before the first is coded;
+// blockIdx.y picks K or V.
+template <int D, int GROUP, bool BF16, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendParams p) {
   constexpr int kChunks = D / 8;  // of a row: 8 or 16, so a warp holds whole rows
   constexpr int T = D / 32;
   const bool is_v = blockIdx.y != 0;
   const uint32_t per_token = p.pool.hk * kChunks;
   const uint32_t chunks = static_cast<uint32_t>(p.n) * per_token;
-  const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
-  const bool live = i < chunks;
-  const uint32_t token = live ? i / per_token : 0u;
-  const uint32_t in_token = live ? i - token * per_token : 0u;
-  const int slot = live ? __ldg(p.slots + token) : -1;
-  const bool ok = slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
-  uint4 u = make_uint4(0u, 0u, 0u, 0u);
-  if (ok)
-    u = __ldg(reinterpret_cast<const uint4*>((is_v ? p.v + token * p.v_stride
-                                                   : p.k + token * p.k_stride) +
-                                             in_token * 16));
-  uint32_t a = kv4::absmax_bits(u);
+  const uint8_t* const src = is_v ? p.v : p.k;
+  const int64_t stride = is_v ? p.v_stride : p.k_stride;
+  const uint32_t i0 = blockIdx.x * (U * kRowThreads) + threadIdx.x;
+  uint4 data[U];
+  int slots[U];
 #pragma unroll
-  for (int by = GROUP / 16; by > 0; by >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, by));
-  const bool finite = a < kv4::kInfBits<BF16>;
-  const uint32_t sbits =
-      finite ? kv4::pack1<BF16>(kv4::unpack1<BF16>(a) * (1.0f / 7.0f)) : kv4::kInfBits<BF16> + 1u;
-  // 4096 / s; a bfloat16 s below 2^-100 is lifted first, so that it stays finite
-  const float s = finite ? kv4::unpack1<BF16>(sbits) : 0.f;
-  const float up = BF16 && s < 0x1p-100f ? 0x1p64f : 1.0f;
-  const float r = s > 0.f ? __frcp_rn(s * up) * 4096.0f : 0.f;
-  uint32_t word = finite ? kv4::code_word<BF16>(u, r, up) : 0x88888888u;
-  const int head = in_token / kChunks, w = in_token % kChunks;
-  const size_t row = ((static_cast<size_t>(slot >> p.pool.page_shift) * p.pool.hk + head)
-                      << p.pool.page_shift) +
-                     (slot & ((1 << p.pool.page_shift) - 1));
-  int place;
-  if (!is_v) {
-    place = kv4::k_place<D>(w);
-  } else {
-    // V's halfwords 2w and 2w + 1 lie apart: halfword 8t + g at place g T + t.
-    // The lane four on holds the same places of the next t: each of the two
-    // lanes sends one half and keeps a whole 32-bit word.
-    const int t = w >> 2;
-    const uint32_t other =
-        __shfl_xor_sync(0xffffffffu, (t & 1) ? word & 0xffffu : word >> 16, 4);
-    const int g = 2 * (w & 3) + (t & 1);
-    word = (t & 1) ? __byte_perm(other, word, 0x7610) : __byte_perm(word, other, 0x5410);
-    place = g * (T / 2) + (t >> 1);
+  for (int x = 0; x < U; ++x) {
+    const uint32_t i = min(i0 + x * kRowThreads, chunks - 1);
+    const uint32_t token = i / per_token;
+    data[x] = __ldg(reinterpret_cast<const uint4*>(src + token * stride + (i - token * per_token) * 16));
+    slots[x] = __ldg(p.slots + token);
   }
-  if (ok) {
-    uint8_t* codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + row * (D / 2);
-    *reinterpret_cast<uint32_t*>(codes + place * 4) = word;
-    if (w % (GROUP / 8) == 0) {
-      uint8_t* scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + row * (2 * (D / GROUP));
-      *reinterpret_cast<unsigned short*>(scales + 2 * (w / (GROUP / 8))) =
-          static_cast<unsigned short>(sbits);
+#pragma unroll
+  for (int x = 0; x < U; ++x) {
+    const uint32_t i = i0 + x * kRowThreads;
+    const bool live = i < chunks;
+    const uint32_t in_token = live ? i % per_token : 0u;
+    const int slot = slots[x];
+    const bool ok = live && slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
+    const uint4 u = data[x];
+    uint32_t a = kv4::absmax_bits(u);
+#pragma unroll
+    for (int by = GROUP / 16; by > 0; by >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, by));
+    const bool finite = a < kv4::kInfBits<BF16>;
+    const uint32_t sbits = finite ? kv4::pack1<BF16>(kv4::unpack1<BF16>(a) * (1.0f / 7.0f))
+                                  : kv4::kInfBits<BF16> + 1u;
+    // 4096 / s; a bfloat16 s below 2^-100 is lifted first, so that it stays finite
+    const float s = finite ? kv4::unpack1<BF16>(sbits) : 0.f;
+    const float up = BF16 && s < 0x1p-100f ? 0x1p64f : 1.0f;
+    const float r = s > 0.f ? __frcp_rn(s * up) * 4096.0f : 0.f;
+    uint32_t word = finite ? kv4::code_word<BF16>(u, r, up) : 0x88888888u;
+    const int head = in_token / kChunks, w = in_token % kChunks;
+    int place;
+    if (!is_v) {
+      place = kv4::k_place<D>(w);
+    } else {
+      // V's halfwords 2w and 2w + 1 lie apart: halfword 8t + g at place g T + t.
+      // The lane four on holds the same places of the next t: each of the two
+      // lanes sends one half and keeps a whole 32-bit word.
+      const int t = w >> 2;
+      const uint32_t other =
+          __shfl_xor_sync(0xffffffffu, (t & 1) ? word & 0xffffu : word >> 16, 4);
+      const int g = 2 * (w & 3) + (t & 1);
+      word = (t & 1) ? __byte_perm(other, word, 0x7610) : __byte_perm(word, other, 0x5410);
+      place = g * (T / 2) + (t >> 1);
     }
-  } else if (live && slot != -1) {
-    atomicOr(&g_kv4_status, kStatusBadPages);
+    if (ok) {
+      const size_t row = ((static_cast<size_t>(slot >> p.pool.page_shift) * p.pool.hk + head)
+                          << p.pool.page_shift) +
+                         (slot & ((1 << p.pool.page_shift) - 1));
+      uint8_t* codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + row * (D / 2);
+      *reinterpret_cast<uint32_t*>(codes + place * 4) = word;
+      if (w % (GROUP / 8) == 0) {
+        uint8_t* scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + row * (2 * (D / GROUP));
+        *reinterpret_cast<unsigned short*>(scales + 2 * (w / (GROUP / 8))) =
+            static_cast<unsigned short>(sbits);
+      }
+    } else if (live && slot != -1) {
+      atomicOr(&g_kv4_status, kStatusBadPages);
+    }
   }
 }
 
-// blockIdx.y: sequence; blockIdx.z: K or V; the CTAs of blockIdx.x
-// stride over the sequence's chunks.
-template <int D, int GROUP, bool BF16>
+// blockIdx.y: sequence; blockIdx.z: K or V; the CTAs of blockIdx.x stride over
+// the sequence's chunks, U of a thread at a time.  A thread takes the 32-bit word
+// at its own place of a row (of V, half of two words: it exchanges one with the
+// lane that has their other halves).
+template <int D, int GROUP, bool BF16, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherParams p) {
   constexpr int kChunks = D / 8;
   constexpr int T = D / 32;
@@ -180,48 +196,76 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
   const uint8_t* scales = is_v ? p.pool.v_scale : p.pool.k_scale;
   uint8_t* out = is_v ? p.v : p.k;
   const int32_t* table = p.block_table + static_cast<size_t>(s) * p.max_pages;
-  // token and chunk of the token, carried along without a division per step
-  const uint32_t first = blockIdx.x * kRowThreads + threadIdx.x;
-  const uint32_t step = gridDim.x * kRowThreads;  // < 2^25
-  const uint32_t step_pos = step / per_token, step_in = step % per_token;
+  // token and place in the token, carried along without a division per step
+  const uint32_t first = blockIdx.x * (U * kRowThreads) + threadIdx.x;
+  const uint32_t hop_pos = kRowThreads / per_token, hop_in = kRowThreads % per_token;
+  const uint32_t far = (gridDim.x - 1) * (U * kRowThreads);  // < 2^25, beyond the U hops
+  const uint32_t far_pos = far / per_token, far_in = far % per_token;
   uint32_t in_next = first % per_token;
   long long pos_next = first / per_token;
-  while (pos_next < len) {
-    const uint32_t pos = static_cast<uint32_t>(pos_next), in_token = in_next;
-    pos_next += step_pos;
-    in_next += step_in;
+  const auto forth = [&](uint32_t by_pos, uint32_t by_in) {
+    pos_next += by_pos;
+    in_next += by_in;
     if (in_next >= per_token) {
       in_next -= per_token;
       ++pos_next;
     }
-    const int page = __ldg(table + (pos >> sh));
-    const long long to = out0 + pos;
-    if (page < 0 || page >= p.pool.num_pages || to < 0 || to >= p.rows) {
-      bad = true;
-      continue;
-    }
-    const int head = in_token / kChunks, w = in_token % kChunks;
-    const size_t row =
-        ((static_cast<size_t>(page) * p.pool.hk + head) << sh) + (pos & ((1u << sh) - 1));
-    uint32_t word;
-    if (!is_v) {
-      word = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + kv4::k_place<D>(w));
-    } else {
-      const unsigned short* h = reinterpret_cast<const unsigned short*>(codes + row * (D / 2)) +
-                                2 * (w & 3) * T + (w >> 2);
-      word = __ldg(h) | (static_cast<uint32_t>(__ldg(h + T)) << 16);
-    }
-    const float sc = kv4::unpack1<BF16>(__ldg(
-        reinterpret_cast<const unsigned short*>(scales + row * (2 * (D / GROUP))) + w / (GROUP / 8)));
-    uint32_t o[4];
+  };
+  // the whole warp goes on while one of its lanes has a token left
+  while (__any_sync(0xffffffffu, pos_next < len)) {
+    uint32_t in_token[U], word[U], scale[U];
+    int pos[U], page[U];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float lo = static_cast<float>(static_cast<int>((word >> (8 * k)) & 15u) - 8);
-      const float hi = static_cast<float>(static_cast<int>((word >> (8 * k + 4)) & 15u) - 8);
-      o[k] = kv4::pack2<BF16>(lo * sc, hi * sc);
+    for (int x = 0; x < U; ++x) {
+      in_token[x] = in_next;
+      pos[x] = pos_next < len ? static_cast<int>(pos_next) : -1;
+      page[x] = pos[x] >= 0 ? __ldg(table + (pos[x] >> sh)) : 0;
+      forth(hop_pos, hop_in);
     }
-    *reinterpret_cast<uint4*>(out + (static_cast<size_t>(to) * per_token + in_token) * 16) =
-        make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const long long to = out0 + pos[x];
+      if (pos[x] >= 0 && (page[x] < 0 || page[x] >= p.pool.num_pages || to < 0 || to >= p.rows)) {
+        bad = true;
+        pos[x] = -1;
+      }
+      word[x] = scale[x] = 0u;
+      if (pos[x] >= 0) {
+        const int head = in_token[x] / kChunks, at = in_token[x] % kChunks;
+        const size_t row =
+            ((static_cast<size_t>(page[x]) * p.pool.hk + head) << sh) + (pos[x] & ((1 << sh) - 1));
+        word[x] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + at);
+        // K: place q T + t holds word 4t + q; V: place g (T / 2) + t / 2 makes, with the
+        // lane of g ^ 1, words 4t + g / 2 of both t, of which it keeps t + (g & 1)
+        const int w = is_v ? 4 * (2 * (at % (T / 2)) + (at / (T / 2) & 1)) + at / T
+                           : 4 * (at % T) + at / T;
+        scale[x] = __ldg(reinterpret_cast<const unsigned short*>(scales + row * (2 * (D / GROUP))) +
+                         w / (GROUP / 8));
+        in_token[x] += w - at;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      uint32_t v = word[x];
+      if (is_v) {
+        // lanes of one row: an even g sends its high half, an odd one its low
+        const bool odd = ((threadIdx.x % kChunks) / (T / 2)) & 1;
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v & 0xffffu : v >> 16, T / 2);
+        v = odd ? __byte_perm(other, v, 0x7610) : __byte_perm(v, other, 0x5410);
+      }
+      if (pos[x] < 0) continue;
+      const float sc = kv4::unpack1<BF16>(scale[x]);
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float lo = static_cast<float>(static_cast<int>((v >> (8 * k)) & 15u) - 8);
+        const float hi = static_cast<float>(static_cast<int>((v >> (8 * k + 4)) & 15u) - 8);
+        o[k] = kv4::pack2<BF16>(lo * sc, hi * sc);
+      }
+      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(out0 + pos[x]) * per_token + in_token[x]) * 16) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    forth(far_pos, far_in);
   }
   if (bad) atomicOr(&g_kv4_status, kStatusBadPages);
 }
@@ -246,8 +290,12 @@ struct LaunchAppend {
   template <int D, int GROUP, bool BF16>
   int operator()() const {
     const long long chunks = static_cast<long long>(p.n) * p.pool.hk * (D / 8);
-    const dim3 grid(static_cast<unsigned>((chunks + kRowThreads - 1) / kRowThreads), 2);
-    kv4_append_kernel<D, GROUP, BF16><<<grid, kRowThreads, 0, stream>>>(p);
+    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>(chunks) : run<D, GROUP, BF16, 4>(chunks);
+  }
+  template <int D, int GROUP, bool BF16, int U>
+  int run(long long chunks) const {
+    const dim3 grid(static_cast<unsigned>((chunks + U * kRowThreads - 1) / (U * kRowThreads)), 2);
+    kv4_append_kernel<D, GROUP, BF16, U><<<grid, kRowThreads, 0, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }
 };
@@ -260,13 +308,17 @@ struct LaunchGather {
   cudaStream_t stream;
   template <int D, int GROUP, bool BF16>
   int operator()() const {
-    // about 32 resident CTAs' worth per SM over all sequences
-    const long long most = static_cast<long long>(p.rows) * p.pool.hk * (D / 8);
-    long long per_seq = (most / p.nseq + kRowThreads - 1) / kRowThreads;
+    const long long chunks = static_cast<long long>(p.rows) * p.pool.hk * (D / 8);
+    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>(chunks) : run<D, GROUP, BF16, 4>(chunks);
+  }
+  template <int D, int GROUP, bool BF16, int U>
+  int run(long long chunks) const {
+    // one sweep of a sequence of the average length
+    long long per_seq = (chunks / p.nseq + U * kRowThreads - 1) / (U * kRowThreads);
     if (per_seq < 1) per_seq = 1;
-    if (per_seq > 65535) per_seq = 65535;
+    if (per_seq > 16384) per_seq = 16384;
     const dim3 grid(static_cast<unsigned>(per_seq), p.nseq, 2);
-    kv4_gather_kernel<D, GROUP, BF16><<<grid, kRowThreads, 0, stream>>>(p);
+    kv4_gather_kernel<D, GROUP, BF16, U><<<grid, kRowThreads, 0, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }
 };

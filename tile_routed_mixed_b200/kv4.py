@@ -13,6 +13,7 @@ and none of it reads anything back to the host.
 from __future__ import annotations
 
 import ctypes
+import threading
 from typing import NamedTuple
 
 import torch
@@ -27,6 +28,12 @@ class PagePlan(NamedTuple):
     token_start: torch.Tensor
     slots: torch.Tensor
     granted: torch.Tensor
+
+
+_stream_of = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
+_device_now = torch._C._cuda_getDevice
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+_i32 = torch.int32
 
 
 def _dtype_id(dtype):
@@ -70,7 +77,7 @@ class TileMixKV4Cache:
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
-        dev, i32 = self.device, torch.int32
+        dev = self.device
         rows = (self.num_pages, self.hk, self.page_size)
         shapes = [(rows + (self.d // 2,), torch.uint8), (rows + (self.d // self.group,), dtype)] * 2
         dt = _dtype_id(dtype)
@@ -78,13 +85,13 @@ class TileMixKV4Cache:
             pool = [torch.zeros(s, dtype=t, device=dev) for s, t in shapes]
         for x, (s, t) in zip(pool, shapes, strict=True):
             self._expect(x, t, s, "pool")
-        shapes = [((self.max_seqs, self.max_pages), i32), ((self.max_seqs,), i32),
-                  ((self.num_pages,), i32), ((1,), i32)]
+        shapes = [((self.max_seqs, self.max_pages), _i32), ((self.max_seqs,), _i32),
+                  ((self.num_pages,), _i32), ((1,), _i32)]
         if tables is None:
-            tables = (torch.full(shapes[0][0], -1, dtype=i32, device=dev),
-                      torch.zeros(self.max_seqs, dtype=i32, device=dev),
-                      torch.arange(self.num_pages - 1, -1, -1, dtype=i32, device=dev),
-                      torch.full((1,), self.num_pages, dtype=i32, device=dev))
+            tables = (torch.full(shapes[0][0], -1, dtype=_i32, device=dev),
+                      torch.zeros(self.max_seqs, dtype=_i32, device=dev),
+                      torch.arange(self.num_pages - 1, -1, -1, dtype=_i32, device=dev),
+                      torch.full((1,), self.num_pages, dtype=_i32, device=dev))
         for x, (s, t) in zip(tables, shapes, strict=True):
             self._expect(x, t, s, "tables")
         self.k_codes, self.k_scale, self.v_codes, self.v_scale = pool
@@ -112,42 +119,46 @@ class TileMixKV4Cache:
             "tilemix_kv4_gather": (L.tilemix_kv4_gather, ctypes.byref(self._gather)),
             "tilemix_kv4_attn": (L.tilemix_kv4_attn, ctypes.byref(self._attn)),
         }
+        self._lock = threading.Lock()  # on the blocks: a call fills one and enqueues it
         self._spaces = {}
+        self._f32 = torch.empty(0, dtype=torch.float32, device=dev)
 
     # ---------------------------------------------------------------- checks
 
-    def _expect(self, x, dtype, shape, what):
-        """x is a contiguous tensor of this device; a None in shape matches any size."""
-        if x.dtype is dtype and x.get_device() == self._index and x.is_contiguous():
-            have = x.shape
-            if have == shape or (len(have) == len(shape) and
-                                 all(n is None or a == n for a, n in zip(have, shape))):
-                return
+    def _refuse(self, what, x, dtype, shape):
         raise ValueError("%s: expected a contiguous %s tensor of shape %s on %s, got %s %s on %s"
                          % (what, dtype, tuple(shape), self.device, x.dtype, tuple(x.shape), x.device))
 
-    def _nseq(self, x, what, extra=0):
-        n = x.shape[0] - extra
+    def _expect(self, x, dtype, shape, what):
+        """x is a contiguous tensor of this device, of that type and shape."""
+        if not (x.dtype is dtype and x.get_device() == self._index and x.shape == shape
+                and x.is_contiguous()):
+            self._refuse(what, x, dtype, shape)
+
+    def _vector(self, x, what, extra=0):
+        """Entries of an int32 vector with one for each sequence (and `extra`)."""
+        shape = x.shape
+        if not (x.dtype is _i32 and x.get_device() == self._index and len(shape) == 1
+                and x.is_contiguous()):
+            self._refuse(what, x, _i32, ("nseq",))
+        n = shape[0] - extra
         if not 0 <= n <= self.max_seqs:
             raise ValueError("%s: the cache holds %d sequences" % (what, self.max_seqs))
         return n
 
-    def _on(self, stream, fn, *args):
-        """fn(*args, raw stream) with this object's device, and `stream`, current."""
-        if stream is not None:
-            if stream.device != self.device:
-                raise ValueError("the stream belongs to %s, the cache to %s" % (stream.device, self.device))
-            with torch.cuda.stream(stream):
-                return fn(*args, stream.cuda_stream)
-        index = self._index
-        if torch.cuda.current_device() != index:
-            with torch.cuda.device(index):
-                return fn(*args, torch.cuda.current_stream(index).cuda_stream)
-        return fn(*args, torch.cuda.current_stream(index).cuda_stream)
+    def _elsewhere(self, stream, fn, *args):
+        """fn(*args) with this object's device, and `stream`, current."""
+        if stream is None:
+            with torch.cuda.device(self._index):
+                return fn(*args)
+        if stream.device != self.device:
+            raise ValueError("the stream belongs to %s, the cache to %s" % (stream.device, self.device))
+        with torch.cuda.stream(stream):
+            return fn(*args)
 
-    def _call(self, name, stream):
+    def _call(self, name):
         fn, args = self._calls[name]
-        rc = fn(args, stream)
+        rc = fn(args, _stream_of(self._index))
         if rc:
             _check(rc, name)
 
@@ -156,60 +167,60 @@ class TileMixKV4Cache:
     def new_plan(self, max_tokens, nseq=None):
         """Buffers of a plan, for plan(out=...)."""
         n = self.max_seqs if nseq is None else int(nseq)
-        new = lambda m: torch.empty(m, dtype=torch.int32, device=self.device)
+        new = lambda m: torch.empty(m, dtype=_i32, device=self.device)
         return PagePlan(new(n + 1), new(int(max_tokens)), new(n))
 
     def plan(self, new_len, max_tokens=None, out=None, stream=None):
         """Pages and slots for new_len[s] more tokens (fewer, if negative) of each
         sequence (see tilemix_page_plan).  new_len: int32 [nseq] on the device;
         max_tokens: the number of slots, or `out` from new_plan()."""
-        return self._on(stream, self._plan_call, new_len, max_tokens, out)
-
-    def _plan_call(self, new_len, max_tokens, out, stream):
-        n = self._nseq(new_len, "new_len")
-        self._expect(new_len, torch.int32, (n,), "new_len")
+        if stream is not None or _device_now() != self._index:
+            return self._elsewhere(stream, self.plan, new_len, max_tokens, out)
+        n = self._vector(new_len, "new_len")
         if out is None:
             if max_tokens is None:
                 raise ValueError("max_tokens or out")
             out = self.new_plan(max_tokens, n)
-        else:
-            if max_tokens is not None and max_tokens != out.slots.shape[0]:
-                raise ValueError("max_tokens is %d, out has %d slots" % (max_tokens, out.slots.shape[0]))
-            self._expect(out.token_start, torch.int32, (n + 1,), "token_start")
-            self._expect(out.slots, torch.int32, (None,), "slots")
-            self._expect(out.granted, torch.int32, (n,), "granted")
+        token_start, slots, granted = out
+        tokens = slots.shape[0]
+        self._expect(token_start, _i32, (n + 1,), "token_start")
+        self._expect(slots, _i32, (tokens,), "slots")
+        self._expect(granted, _i32, (n,), "granted")
+        if max_tokens is not None and max_tokens != tokens:
+            raise ValueError("max_tokens is %d, out has %d slots" % (max_tokens, tokens))
         a = self._plan
-        a.new_len, a.nseq = new_len.data_ptr(), n
-        a.token_start, a.granted = out.token_start.data_ptr(), out.granted.data_ptr()
-        a.slots, a.max_tokens = out.slots.data_ptr(), out.slots.shape[0]
-        if n == 0:  # an empty tensor has no address
-            a.new_len = a.granted = out.token_start.data_ptr()
-        self._call("tilemix_page_plan", stream)
+        with self._lock:
+            a.token_start = token_start.data_ptr()
+            # (an empty tensor has no address)
+            a.new_len = new_len.data_ptr() if n else a.token_start
+            a.granted = granted.data_ptr() if n else a.token_start
+            a.slots = slots.data_ptr()
+            a.nseq, a.max_tokens = n, tokens
+            self._call("tilemix_page_plan")
         return out
 
     def append(self, k, v, slots, stream=None):
         """Rows of k and v [n, hk, d] (the heads of a token contiguous, tokens at
         any stride) to slots [n] (int32; -1: skipped)."""
-        return self._on(stream, self._append_call, k, v, slots)
-
-    def _append_call(self, k, v, slots, stream):
+        if stream is not None or _device_now() != self._index:
+            return self._elsewhere(stream, self.append, k, v, slots)
         n = slots.shape[0]
-        self._expect(slots, torch.int32, (n,), "slots")
-        a = self._append
-        a.k_stride, a.v_stride = self._rows(k, n, "k"), self._rows(v, n, "v")
+        self._expect(slots, _i32, (n,), "slots")
+        k_stride, v_stride = self._rows(k, n, "k"), self._rows(v, n, "v")
         if n == 0:
             return
-        a.k, a.v, a.slots, a.n = k.data_ptr(), v.data_ptr(), slots.data_ptr(), n
-        self._call("tilemix_kv4_append", stream)
+        a = self._append
+        with self._lock:
+            a.k, a.v, a.slots, a.n = k.data_ptr(), v.data_ptr(), slots.data_ptr(), n
+            a.k_stride, a.v_stride = k_stride, v_stride
+            self._call("tilemix_kv4_append")
 
     def _rows(self, x, n, what):
         """The stride of x's tokens."""
         shape = x.shape
-        if x.dtype is not self.dtype or x.get_device() != self._index or len(shape) != 3 or \
-                shape[0] < n or shape[1] != self.hk or shape[2] != self.d:
-            raise ValueError("%s: expected %s [%d or more, %d, %d] on %s, got %s %s on %s" %
-                             (what, self.dtype, n, self.hk, self.d, self.device, x.dtype,
-                              tuple(shape), x.device))
+        if not (x.dtype is self.dtype and x.get_device() == self._index and len(shape) == 3
+                and shape[0] >= n and shape[1] == self.hk and shape[2] == self.d):
+            self._refuse(what, x, self.dtype, ("%d or more" % n, self.hk, self.d))
         token, head, channel = x.stride()
         if channel != 1 or (self.hk > 1 and head != self.d):
             raise ValueError("%s: a token's heads must be contiguous" % what)
@@ -218,24 +229,22 @@ class TileMixKV4Cache:
     def gather(self, out_start, rows, out=None, stream=None):
         """K and V of the sequences' tokens as 16-bit values: position p of
         sequence s at row out_start[s] + p (int32 [nseq]) of two [rows, hk, d]
-        tensors (`out`, or new ones)."""
-        return self._on(stream, self._gather_call, out_start, rows, out)
-
-    def _gather_call(self, out_start, rows, out, stream):
-        n = self._nseq(out_start, "out_start")
-        self._expect(out_start, torch.int32, (n,), "out_start")
+        tensors (`out`, or new ones, whose other rows hold nothing meaningful)."""
+        if stream is not None or _device_now() != self._index:
+            return self._elsewhere(stream, self.gather, out_start, rows, out)
+        n = self._vector(out_start, "out_start")
         rows = int(rows)
-        shape = (rows, self.hk, self.d)
         if out is None:
-            out = (torch.empty(shape, dtype=self.dtype, device=self.device),
-                   torch.empty(shape, dtype=self.dtype, device=self.device))
+            new = self.k_scale.new_empty
+            out = new(rows, self.hk, self.d), new(rows, self.hk, self.d)
         else:
             for x in out:
-                self._expect(x, self.dtype, shape, "out")
+                self._expect(x, self.dtype, (rows, self.hk, self.d), "out")
         a = self._gather
-        a.out_start, a.nseq, a.rows = out_start.data_ptr(), n, rows
-        a.k, a.v = out[0].data_ptr(), out[1].data_ptr()
-        self._call("tilemix_kv4_gather", stream)
+        with self._lock:
+            a.out_start, a.nseq, a.rows = out_start.data_ptr(), n, rows
+            a.k, a.v = out[0].data_ptr(), out[1].data_ptr()
+            self._call("tilemix_kv4_gather")
         return tuple(out)
 
     def attend(self, q, max_seqlen, token_start=None, max_new=1, softmax_scale=0.0, out=None,
@@ -247,52 +256,56 @@ class TileMixKV4Cache:
         sequence.  Returns o like q, or (o, LSE [hq, rows]) if lse; `out` and a
         tensor as `lse` are written in place.  Rows that no sequence covers are
         not written (in a new tensor they hold nothing meaningful)."""
-        return self._on(stream, self._attend_call, q, max_seqlen, token_start, max_new,
-                        softmax_scale, out, lse)
-
-    def _attend_call(self, q, max_seqlen, token_start, max_new, softmax_scale, out, lse, stream):
-        self._expect(q, self.dtype, (None, None, self.d), "q")
-        rows, hq = q.shape[0], q.shape[1]
+        if stream is not None or _device_now() != self._index:
+            return self._elsewhere(stream, self.attend, q, max_seqlen, token_start, max_new,
+                                   softmax_scale, out, lse)
+        shape = q.shape
+        if not (q.dtype is self.dtype and q.get_device() == self._index and len(shape) == 3
+                and shape[2] == self.d and q.is_contiguous()):
+            self._refuse("q", q, self.dtype, ("rows", "hq", self.d))
+        rows, hq, _ = shape
         if hq < 1 or hq % self.hk != 0:
             raise ValueError("q has %d heads, the cache %d" % (hq, self.hk))
-        a = self._attn
         if token_start is None:
-            n = self._nseq(q, "q")
-            a.token_start = None
+            n, start = rows, None
+            if n > self.max_seqs:
+                raise ValueError("q: the cache holds %d sequences" % self.max_seqs)
         else:
-            n = self._nseq(token_start, "token_start", 1)
-            self._expect(token_start, torch.int32, (n + 1,), "token_start")
-            a.token_start = token_start.data_ptr()
+            n, start = self._vector(token_start, "token_start", 1), token_start.data_ptr()
         if out is None:
             out = torch.empty_like(q)
         else:
-            self._expect(out, self.dtype, q.shape, "out")
-        want = lse is not None and lse is not False
+            self._expect(out, self.dtype, shape, "out")
         if lse is True:
-            lse = torch.empty((hq, rows), dtype=torch.float32, device=self.device)
-        elif want:
+            lse = self._f32.new_empty(hq, rows)
+        elif lse is not None and lse is not False:
             self._expect(lse, torch.float32, (hq, rows), "lse")
-        a.q, a.o = q.data_ptr(), out.data_ptr()
-        a.lse = lse.data_ptr() if want else None
-        a.nseq, a.total_q, a.hq = n, rows, hq
-        a.max_new, a.max_seqlen, a.softmax_scale = int(max_new), int(max_seqlen), float(softmax_scale)
-        if rows and n:
-            # kept until the call is enqueued: a graph's own lives in its pool from then on
-            work, sync, a.workspace, a.workspace_bytes, a.sync = self._space(a, stream)
-            self._call("tilemix_kv4_attn", stream)
-        return (out, lse) if want else out
+        else:
+            lse = None
+        a = self._attn
+        with self._lock:
+            a.q, a.o, a.token_start = q.data_ptr(), out.data_ptr(), start
+            a.lse = None if lse is None else lse.data_ptr()
+            a.nseq, a.total_q, a.hq = n, rows, hq
+            a.max_new, a.max_seqlen, a.softmax_scale = max_new, max_seqlen, softmax_scale
+            if rows and n:
+                # (held until the call is enqueued: a graph's own lives in its pool from then on)
+                space = self._space(a, max_new * hq > 8 * self.hk)
+                a.workspace, a.workspace_bytes, a.sync = space[2:]
+            self._call("tilemix_kv4_attn")
+        return out if lse is None else (out, lse)
 
-    def _space(self, a, stream):
-        """Workspace and sync words of a stream, and their addresses and size."""
-        key = (stream, a.max_new * a.hq > 8 * self.hk)
+    def _space(self, a, wide):
+        """Workspace and sync words of the current stream, their addresses and size."""
+        key = _stream_of(self._index), wide
         space = self._spaces.get(key)
-        if space is not None and not torch.cuda.is_current_stream_capturing():
+        if space is not None and not _capturing():
             return space
         # a graph being captured gets one of its own: its replays must not share
         # one with calls outside it
         work = torch.empty(tilemix_kv4_attn_workspace_size(a), dtype=torch.uint8, device=self.device)
-        sync = torch.zeros(KV4_SYNC_WORDS, dtype=torch.int32, device=self.device)
+        sync = torch.zeros(KV4_SYNC_WORDS, dtype=_i32, device=self.device)
         space = (work, sync, work.data_ptr(), work.shape[0], sync.data_ptr())
-        if not torch.cuda.is_current_stream_capturing():
+        if not _capturing():
             self._spaces[key] = space
         return space

@@ -88,23 +88,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The codes of nibbles I (0: the low one) of both halves of a word, as fp16.
-__device__ __forceinline__ uint32_t or_1024(uint32_t x, uint32_t mask) {  // (x & mask) | 0x64006400
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(x), "r"(mask));
-  return y;
-}
-__device__ __forceinline__ uint32_t code_low(uint32_t x) {  // bits 0 .. 3: 1024 + u - 1032
-  uint32_t y = or_1024(x, 0x000F000Fu);
-  asm("add.f16x2 %0, %0, %1;" : "+r"(y) : "r"(0xE408E408u));
-  return y;
-}
-__device__ __forceinline__ uint32_t code_high(uint32_t x) {  // bits 4 .. 7: (1024 + 16 u) / 16 - 72
-  uint32_t y = or_1024(x, 0x00F000F0u);
-  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x2C002C00u), "r"(0xD480D480u));
-  return y;
-}
-
 // D[16x8] = A[16x16] * B[16x8], fp16 inputs, fp32 sums from zero.
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                               uint32_t b1) {

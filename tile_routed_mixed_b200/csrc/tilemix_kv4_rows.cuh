@@ -27,6 +27,23 @@ constexpr long long kRowsWide = 148LL * 2048 * 2;
 
 namespace kv4 {
 
+// The codes of nibbles in both halves of a word, as fp16 pairs.
+__device__ __forceinline__ uint32_t or_1024(uint32_t x, uint32_t mask) {  // (x & mask) | 0x64006400
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, 0x64006400, 0xEA;" : "=r"(y) : "r"(x), "r"(mask));
+  return y;
+}
+__device__ __forceinline__ uint32_t code_low(uint32_t x) {  // bits 0 .. 3: 1024 + u - 1032
+  uint32_t y = or_1024(x, 0x000F000Fu);
+  asm("add.f16x2 %0, %0, %1;" : "+r"(y) : "r"(0xE408E408u));
+  return y;
+}
+__device__ __forceinline__ uint32_t code_high(uint32_t x) {  // bits 4 .. 7: (1024 + 16 u) / 16 - 72
+  uint32_t y = or_1024(x, 0x00F000F0u);
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x2C002C00u), "r"(0xD480D480u));
+  return y;
+}
+
 // Two packed values of the activations' type to fp32.
 template <bool BF16>
 __device__ __forceinline__ float2 unpack2(uint32_t u) {
@@ -71,29 +88,55 @@ __device__ __forceinline__ uint32_t absmax_bits(const uint4& u) {
   return max(a & 0xffffu, a >> 16);
 }
 
-// The eight codes + 8 of a chunk as nibbles, channel 0 lowest.  r = 4096 / s
-// (0 for s = 0), up = 1 or the power of two that r's s was multiplied by.
+// The eight codes + 8 of a chunk as nibbles, channel 0 lowest.  r = 4096 / s (0
+// for s = 0).  RARE: s is subnormal (or zero); quotients may then lie beyond
+// +-7, and up is the power of two that r's s was multiplied by.
 constexpr float kShift = 12582912.0f;  // 1.5 * 2^23: x + kShift is rne(x) + kShift
-template <bool BF16>
+template <bool BF16, bool RARE>
 __device__ __forceinline__ uint32_t code_word(const uint4& u, float r, float up) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  float c[8];
+  uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = unpack2<BF16>(w[i]);
-    c[2 * i] = x.x * up;
-    c[2 * i + 1] = x.y * up;
-  }
-  uint32_t word = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // 4096 x / s, rounded to an integer; beyond +-7 only where s is subnormal
-    const float t = fminf(fmaxf(fmaf(c[i], r, kShift) - kShift, -28672.0f), 28672.0f);
-    // its 2^-12th, rounded to an integer, + 8, in the low bits of the sum
-    const uint32_t b = __float_as_uint(fmaf(t, 0x1p-12f, kShift + 8.0f));
-    word |= (b & 15u) << (4 * i);
+    for (int j = 0; j < 2; ++j) {
+      const float c = (j ? x.y : x.x) * (RARE ? up : 1.0f);
+      // 4096 x / s, rounded to an integer
+      float t = __fadd_rn(__fmaf_rn(c, r, kShift), -kShift);
+      if (RARE) t = fminf(fmaxf(t, -28672.0f), 28672.0f);
+      // its 2^-12th, rounded to an integer, + 8: the low byte of the sum
+      b[2 * i + j] = __float_as_uint(__fmaf_rn(t, 0x1p-12f, kShift + 8.0f));
+    }
   }
-  return word;
+  const uint32_t even = __byte_perm(__byte_perm(b[0], b[2], 0x0040), __byte_perm(b[4], b[6], 0x0040), 0x5410);
+  const uint32_t odd = __byte_perm(__byte_perm(b[1], b[3], 0x0040), __byte_perm(b[5], b[7], 0x0040), 0x5410);
+  return even + (odd << 4);
+}
+
+// The eight values of a word of codes, scaled: the product of a code and a
+// scale in the type itself is rounded once.
+template <bool BF16>
+__device__ __forceinline__ uint4 values_of(uint32_t w, uint32_t scale) {
+  const uint32_t s2 = scale | (scale << 16);
+  uint32_t p[4];  // channels i and i + 4
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // 128 + u, less 136
+      uint32_t c = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(c) : "r"(0xC308C308u));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(s2));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = (i & 1) ? code_high(w >> (8 * (i / 2))) : code_low(w >> (8 * (i / 2)));
+      asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p[i]) : "r"(c), "r"(s2));
+    }
+  }
+  return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                    __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
 }
 
 // Place of a row's 32-bit word of K holding channels 8w .. 8w + 7.
@@ -112,26 +155,33 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
   constexpr int T = D / 32;
   const bool is_v = blockIdx.y != 0;
   const uint32_t per_token = p.pool.hk * kChunks;
-  const uint32_t chunks = static_cast<uint32_t>(p.n) * per_token;
   const uint8_t* const src = is_v ? p.v : p.k;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
   const uint32_t i0 = blockIdx.x * (U * kRowThreads) + threadIdx.x;
+  uint32_t token = i0 / per_token, within = i0 - token * per_token;
+  const uint32_t hop = kRowThreads / per_token, hop_in = kRowThreads % per_token;
   uint4 data[U];
   int slots[U];
+  uint32_t in_token_of[U];
 #pragma unroll
   for (int x = 0; x < U; ++x) {
-    const uint32_t i = min(i0 + x * kRowThreads, chunks - 1);
-    const uint32_t token = i / per_token;
-    data[x] = __ldg(reinterpret_cast<const uint4*>(src + token * stride + (i - token * per_token) * 16));
-    slots[x] = __ldg(p.slots + token);
+    const bool live = token < static_cast<uint32_t>(p.n);
+    in_token_of[x] = live ? within : 0u;
+    const uint32_t from = live ? token : static_cast<uint32_t>(p.n) - 1;
+    data[x] = __ldg(reinterpret_cast<const uint4*>(src + from * stride + in_token_of[x] * 16));
+    slots[x] = live ? __ldg(p.slots + from) : -1;
+    token += hop;
+    within += hop_in;
+    if (within >= per_token) {
+      within -= per_token;
+      ++token;
+    }
   }
 #pragma unroll
   for (int x = 0; x < U; ++x) {
-    const uint32_t i = i0 + x * kRowThreads;
-    const bool live = i < chunks;
-    const uint32_t in_token = live ? i % per_token : 0u;
+    const uint32_t in_token = in_token_of[x];
     const int slot = slots[x];
-    const bool ok = live && slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
+    const bool ok = slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
     const uint4 u = data[x];
     uint32_t a = kv4::absmax_bits(u);
 #pragma unroll
@@ -139,11 +189,15 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     const bool finite = a < kv4::kInfBits<BF16>;
     const uint32_t sbits = finite ? kv4::pack1<BF16>(kv4::unpack1<BF16>(a) * (1.0f / 7.0f))
                                   : kv4::kInfBits<BF16> + 1u;
-    // 4096 / s; a bfloat16 s below 2^-100 is lifted first, so that it stays finite
-    const float s = finite ? kv4::unpack1<BF16>(sbits) : 0.f;
-    const float up = BF16 && s < 0x1p-100f ? 0x1p64f : 1.0f;
-    const float r = s > 0.f ? __frcp_rn(s * up) * 4096.0f : 0.f;
-    uint32_t word = finite ? kv4::code_word<BF16>(u, r, up) : 0x88888888u;
+    uint32_t word = 0x88888888u;
+    if (sbits >= (BF16 ? 0x0e00u : 0x0400u)) {
+      // s >= 2^-99 (2^-14), normal; a NaN s takes this way too, with codes of 0
+      const float r = finite ? __frcp_rn(kv4::unpack1<BF16>(sbits)) * 4096.0f : 0.f;
+      word = kv4::code_word<BF16, false>(finite ? u : make_uint4(0u, 0u, 0u, 0u), r, 1.0f);
+    } else if (sbits != 0) {
+      const float up = BF16 ? 0x1p64f : 1.0f;  // so that 4096 / s stays finite
+      word = kv4::code_word<BF16, true>(u, __frcp_rn(kv4::unpack1<BF16>(sbits) * up) * 4096.0f, up);
+    }
     const int head = in_token / kChunks, w = in_token % kChunks;
     int place;
     if (!is_v) {
@@ -170,7 +224,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
         *reinterpret_cast<unsigned short*>(scales + 2 * (w / (GROUP / 8))) =
             static_cast<unsigned short>(sbits);
       }
-    } else if (live && slot != -1) {
+    } else if (slot != -1) {
       atomicOr(&g_kv4_status, kStatusBadPages);
     }
   }
@@ -254,16 +308,8 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
         v = odd ? __byte_perm(other, v, 0x7610) : __byte_perm(v, other, 0x5410);
       }
       if (pos[x] < 0) continue;
-      const float sc = kv4::unpack1<BF16>(scale[x]);
-      uint32_t o[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float lo = static_cast<float>(static_cast<int>((v >> (8 * k)) & 15u) - 8);
-        const float hi = static_cast<float>(static_cast<int>((v >> (8 * k + 4)) & 15u) - 8);
-        o[k] = kv4::pack2<BF16>(lo * sc, hi * sc);
-      }
       *reinterpret_cast<uint4*>(out + (static_cast<size_t>(out0 + pos[x]) * per_token + in_token[x]) * 16) =
-          make_uint4(o[0], o[1], o[2], o[3]);
+          kv4::values_of<BF16>(v, scale[x]);
     }
     forth(far_pos, far_in);
   }

@@ -541,7 +541,7 @@ typedef struct tilemix_kv4_cache {
   void* v_scale;
   int num_pages;              /* >= 1; num_pages * page_size < 2^31 */
   int page_size;              /* a power of two, 16 .. 1024 */
-  int hk, d;                  /* d in {64, 128} */
+  int hk, d;                  /* hk in 1 .. 32767, d in {64, 128} */
   int group;                  /* 32, 64 or 128, at most d */
   int dtype;                  /* TILEMIX_KV_FP16 or TILEMIX_KV_BF16: the type of the scales
                                  and of every q, k, v and o of these calls */

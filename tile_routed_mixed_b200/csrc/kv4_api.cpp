@@ -30,7 +30,7 @@ int check_cache(const tilemix_kv4_cache& c, bool pointers) {
     return TILEMIX_ERR_UNSUPPORTED;
   if (c.dtype != TILEMIX_KV_FP16 && c.dtype != TILEMIX_KV_BF16) return TILEMIX_ERR_UNSUPPORTED;
   if (page_shift(c.page_size) < 0) return TILEMIX_ERR_UNSUPPORTED;
-  if (c.num_pages < 1 || c.hk < 1 ||
+  if (c.num_pages < 1 || c.hk < 1 || c.hk > 32767 ||
       static_cast<long long>(c.num_pages) * c.page_size > 0x7fffffffLL)
     return TILEMIX_ERR_INVALID_ARG;
   if (!pointers) return TILEMIX_OK;

@@ -1,8 +1,8 @@
 // Rows into and out of the paged 4-bit cache (tilemix_kv4_append,
 // tilemix_kv4_gather).
 //
-// Both are one pass over memory, a thread to each chunk of 8 channels: 16
-// bytes of activations against one 4-byte word of codes.  A group of channels
+// Both are one pass over memory, a thread to a chunk of 8 channels: 16 bytes of
+// activations against one 4-byte word of codes.  A group of channels
 // is 4, 8 or 16 neighbouring lanes, which take its largest magnitude with
 // shuffles; nothing is staged.
 //
@@ -76,6 +76,12 @@ __device__ __forceinline__ uint32_t pack1(float x) {
   else
     return __half_as_ushort(__float2half_rn(x));
 }
+// 1 / x to within an ulp (x normal).
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Bit pattern of the type's infinity: magnitudes from it on are not finite.
 template <bool BF16>
 constexpr uint32_t kInfBits = BF16 ? 0x7f80u : 0x7c00u;
@@ -147,41 +153,41 @@ __device__ __forceinline__ int k_place(int w) {
 
 }  // namespace kv4
 
-// U chunks of 8 channels per thread, all loaded before the first is coded;
-// blockIdx.y picks K or V.
+// A thread has one place of one head's rows (blockIdx.y: head; blockIdx.z: K or
+// V) and U tokens, so that what follows from the place is found once; the U
+// tokens' chunks are all loaded before the first is coded.
 template <int D, int GROUP, bool BF16, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4AppendParams p) {
   constexpr int kChunks = D / 8;  // of a row: 8 or 16, so a warp holds whole rows
-  constexpr int T = D / 32;
-  const bool is_v = blockIdx.y != 0;
-  const uint32_t per_token = p.pool.hk * kChunks;
-  const uint8_t* const src = is_v ? p.v : p.k;
+  constexpr int T = D / 32, kTokens = kRowThreads / kChunks;  // tokens of a sweep
+  const bool is_v = blockIdx.z != 0;
+  const int w = threadIdx.x % kChunks, head = blockIdx.y;
   const int64_t stride = is_v ? p.v_stride : p.k_stride;
-  const uint32_t i0 = blockIdx.x * (U * kRowThreads) + threadIdx.x;
-  uint32_t token = i0 / per_token, within = i0 - token * per_token;
-  const uint32_t hop = kRowThreads / per_token, hop_in = kRowThreads % per_token;
+  const int token0 = blockIdx.x * (U * kTokens) + threadIdx.x / kChunks;
+  const uint8_t* src = (is_v ? p.v : p.k) + (head * kChunks + w) * 16;
   uint4 data[U];
   int slots[U];
-  uint32_t in_token_of[U];
 #pragma unroll
   for (int x = 0; x < U; ++x) {
-    const bool live = token < static_cast<uint32_t>(p.n);
-    in_token_of[x] = live ? within : 0u;
-    const uint32_t from = live ? token : static_cast<uint32_t>(p.n) - 1;
-    data[x] = __ldg(reinterpret_cast<const uint4*>(src + from * stride + in_token_of[x] * 16));
-    slots[x] = live ? __ldg(p.slots + from) : -1;
-    token += hop;
-    within += hop_in;
-    if (within >= per_token) {
-      within -= per_token;
-      ++token;
+    const int token = token0 + x * kTokens;
+    const bool live = token < p.n;
+    data[x] = make_uint4(0u, 0u, 0u, 0u);
+    slots[x] = -1;
+    if (live) {
+      data[x] = __ldg(reinterpret_cast<const uint4*>(src + token * stride));
+      slots[x] = __ldg(p.slots + token);
     }
   }
+  // V's halfwords 2w and 2w + 1 lie apart: halfword 8t + g at place g T + t.  The
+  // lane four on holds the same places of the next t: each of the two lanes sends
+  // one half and keeps a whole 32-bit word.
+  const int t = w >> 2;
+  const int place = is_v ? (2 * (w & 3) + (t & 1)) * (T / 2) + (t >> 1) : kv4::k_place<D>(w);
+  uint8_t* const codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + place * 4;
+  uint8_t* const scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + 2 * (w / (GROUP / 8));
+  const int sh = p.pool.page_shift, in_page = (1 << sh) - 1;
 #pragma unroll
   for (int x = 0; x < U; ++x) {
-    const uint32_t in_token = in_token_of[x];
-    const int slot = slots[x];
-    const bool ok = slot >= 0 && (slot >> p.pool.page_shift) < p.pool.num_pages;
     const uint4 u = data[x];
     uint32_t a = kv4::absmax_bits(u);
 #pragma unroll
@@ -190,112 +196,80 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const Kv4Append
     const uint32_t sbits = finite ? kv4::pack1<BF16>(kv4::unpack1<BF16>(a) * (1.0f / 7.0f))
                                   : kv4::kInfBits<BF16> + 1u;
     uint32_t word = 0x88888888u;
-    if (sbits >= (BF16 ? 0x0e00u : 0x0400u)) {
-      // s >= 2^-99 (2^-14), normal; a NaN s takes this way too, with codes of 0
-      const float r = finite ? __frcp_rn(kv4::unpack1<BF16>(sbits)) * 4096.0f : 0.f;
-      word = kv4::code_word<BF16, false>(finite ? u : make_uint4(0u, 0u, 0u, 0u), r, 1.0f);
-    } else if (sbits != 0) {
+    if (finite && sbits >= (BF16 ? 0x0e00u : 0x0400u)) {  // s >= 2^-99 (2^-14): normal
+      word = kv4::code_word<BF16, false>(u, kv4::rcp(kv4::unpack1<BF16>(sbits)) * 4096.0f, 1.0f);
+    } else if (finite && sbits != 0) {
       const float up = BF16 ? 0x1p64f : 1.0f;  // so that 4096 / s stays finite
-      word = kv4::code_word<BF16, true>(u, __frcp_rn(kv4::unpack1<BF16>(sbits) * up) * 4096.0f, up);
+      word = kv4::code_word<BF16, true>(u, kv4::rcp(kv4::unpack1<BF16>(sbits) * up) * 4096.0f, up);
     }
-    const int head = in_token / kChunks, w = in_token % kChunks;
-    int place;
-    if (!is_v) {
-      place = kv4::k_place<D>(w);
-    } else {
-      // V's halfwords 2w and 2w + 1 lie apart: halfword 8t + g at place g T + t.
-      // The lane four on holds the same places of the next t: each of the two
-      // lanes sends one half and keeps a whole 32-bit word.
-      const int t = w >> 2;
+    if (is_v) {
       const uint32_t other =
           __shfl_xor_sync(0xffffffffu, (t & 1) ? word & 0xffffu : word >> 16, 4);
-      const int g = 2 * (w & 3) + (t & 1);
       word = (t & 1) ? __byte_perm(other, word, 0x7610) : __byte_perm(word, other, 0x5410);
-      place = g * (T / 2) + (t >> 1);
     }
-    if (ok) {
-      const size_t row = ((static_cast<size_t>(slot >> p.pool.page_shift) * p.pool.hk + head)
-                          << p.pool.page_shift) +
-                         (slot & ((1 << p.pool.page_shift) - 1));
-      uint8_t* codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + row * (D / 2);
-      *reinterpret_cast<uint32_t*>(codes + place * 4) = word;
-      if (w % (GROUP / 8) == 0) {
-        uint8_t* scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + row * (2 * (D / GROUP));
-        *reinterpret_cast<unsigned short*>(scales + 2 * (w / (GROUP / 8))) =
+    const int slot = slots[x], page = slot >> sh;  // -1 for -1
+    if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pool.num_pages)) {
+      const int64_t row = ((static_cast<int64_t>(page) * p.pool.hk + head) << sh) + (slot & in_page);
+      *reinterpret_cast<uint32_t*>(codes + row * (D / 2)) = word;
+      if (w % (GROUP / 8) == 0)
+        *reinterpret_cast<unsigned short*>(scales + row * (2 * (D / GROUP))) =
             static_cast<unsigned short>(sbits);
-      }
     } else if (slot != -1) {
       atomicOr(&g_kv4_status, kStatusBadPages);
     }
   }
 }
 
-// blockIdx.y: sequence; blockIdx.z: K or V; the CTAs of blockIdx.x stride over
-// the sequence's chunks, U of a thread at a time.  A thread takes the 32-bit word
-// at its own place of a row (of V, half of two words: it exchanges one with the
-// lane that has their other halves).
+// blockIdx.y: sequence; blockIdx.z: head, K before V; the CTAs of blockIdx.x stride
+// over the sequence's tokens.  A thread takes the 32-bit word at its own place of
+// a row (of V, half of two words: it exchanges one with the lane that has their
+// other halves), U tokens' words before it writes the first.
 template <int D, int GROUP, bool BF16, int U>
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4GatherParams p) {
   constexpr int kChunks = D / 8;
-  constexpr int T = D / 32;
-  const bool is_v = blockIdx.z != 0;
-  const int s = blockIdx.y, sh = p.pool.page_shift;
-  const long long top = static_cast<long long>(p.max_pages) << sh;
+  constexpr int T = D / 32, kTokens = kRowThreads / kChunks;
+  const int hk = p.pool.hk, sh = p.pool.page_shift, in_page = (1 << sh) - 1;
+  const bool is_v = static_cast<int>(blockIdx.z) >= hk;
+  const int head = is_v ? blockIdx.z - hk : blockIdx.z, s = blockIdx.y;
+  const long long top = min(static_cast<long long>(p.max_pages) << sh, 0x7f000000LL);
   const int have = __ldg(p.seq_len + s);
   const int len = static_cast<int>(min(static_cast<long long>(max(have, 0)), top));
-  bool bad = have != len;
   const long long out0 = __ldg(p.out_start + s);
-  const uint32_t per_token = p.pool.hk * kChunks;
-  const uint8_t* codes = is_v ? p.pool.v_codes : p.pool.k_codes;
-  const uint8_t* scales = is_v ? p.pool.v_scale : p.pool.k_scale;
-  uint8_t* out = is_v ? p.v : p.k;
-  const int32_t* table = p.block_table + static_cast<size_t>(s) * p.max_pages;
-  // token and place in the token, carried along without a division per step
-  const uint32_t first = blockIdx.x * (U * kRowThreads) + threadIdx.x;
-  const uint32_t hop_pos = kRowThreads / per_token, hop_in = kRowThreads % per_token;
-  const uint32_t far = (gridDim.x - 1) * (U * kRowThreads);  // < 2^25, beyond the U hops
-  const uint32_t far_pos = far / per_token, far_in = far % per_token;
-  uint32_t in_next = first % per_token;
-  long long pos_next = first / per_token;
-  const auto forth = [&](uint32_t by_pos, uint32_t by_in) {
-    pos_next += by_pos;
-    in_next += by_in;
-    if (in_next >= per_token) {
-      in_next -= per_token;
-      ++pos_next;
-    }
-  };
-  // the whole warp goes on while one of its lanes has a token left
-  while (__any_sync(0xffffffffu, pos_next < len)) {
-    uint32_t in_token[U], word[U], scale[U];
-    int pos[U], page[U];
+  // positions whose rows lie inside the output
+  const int from = static_cast<int>(max(0LL, min(-out0, static_cast<long long>(len))));
+  const int to = static_cast<int>(max(0LL, min(p.rows - out0, static_cast<long long>(len))));
+  bool bad = have != len || from > 0 || to < len;
+  const int at = threadIdx.x % kChunks;
+  // K: place q T + t holds word 4t + q; V: place g (T / 2) + t / 2 makes, with the
+  // lane of g ^ 1, words 4t + g / 2 of both t, of which it keeps t + (g & 1)
+  const bool odd = (at / (T / 2)) & 1;
+  const int w = is_v ? 4 * (2 * (at % (T / 2)) + odd) + at / T : 4 * (at % T) + at / T;
+  const uint8_t* const codes = (is_v ? p.pool.v_codes : p.pool.k_codes) + at * 4;
+  const uint8_t* const scales = (is_v ? p.pool.v_scale : p.pool.k_scale) + 2 * (w / (GROUP / 8));
+  uint8_t* const out = (is_v ? p.v : p.k) + (head * kChunks + w) * 16;
+  const int64_t out_row = static_cast<int64_t>(hk) * (2 * D);
+  const int32_t* const table = p.block_table + static_cast<size_t>(s) * p.max_pages;
+  const int step = gridDim.x * (U * kTokens);
+  for (int base = blockIdx.x * (U * kTokens); base < len; base += step) {
+    const int pos0 = base + threadIdx.x / kChunks;
+    uint32_t word[U], scale[U];
+    int page[U];
 #pragma unroll
     for (int x = 0; x < U; ++x) {
-      in_token[x] = in_next;
-      pos[x] = pos_next < len ? static_cast<int>(pos_next) : -1;
-      page[x] = pos[x] >= 0 ? __ldg(table + (pos[x] >> sh)) : 0;
-      forth(hop_pos, hop_in);
+      const int pos = pos0 + x * kTokens;
+      page[x] = pos >= from && pos < to ? __ldg(table + (pos >> sh)) : -1;
+      if (pos >= from && pos < to) bad |= page[x] < 0 || page[x] >= p.pool.num_pages;
     }
 #pragma unroll
     for (int x = 0; x < U; ++x) {
-      const long long to = out0 + pos[x];
-      if (pos[x] >= 0 && (page[x] < 0 || page[x] >= p.pool.num_pages || to < 0 || to >= p.rows)) {
-        bad = true;
-        pos[x] = -1;
-      }
       word[x] = scale[x] = 0u;
-      if (pos[x] >= 0) {
-        const int head = in_token[x] / kChunks, at = in_token[x] % kChunks;
-        const size_t row =
-            ((static_cast<size_t>(page[x]) * p.pool.hk + head) << sh) + (pos[x] & ((1 << sh) - 1));
-        word[x] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)) + at);
-        // K: place q T + t holds word 4t + q; V: place g (T / 2) + t / 2 makes, with the
-        // lane of g ^ 1, words 4t + g / 2 of both t, of which it keeps t + (g & 1)
-        const int w = is_v ? 4 * (2 * (at % (T / 2)) + (at / (T / 2) & 1)) + at / T
-                           : 4 * (at % T) + at / T;
-        scale[x] = __ldg(reinterpret_cast<const unsigned short*>(scales + row * (2 * (D / GROUP))) +
-                         w / (GROUP / 8));
-        in_token[x] += w - at;
+      if (static_cast<unsigned>(page[x]) < static_cast<unsigned>(p.pool.num_pages)) {
+        const int64_t row = ((static_cast<int64_t>(page[x]) * hk + head) << sh) +
+                            ((pos0 + x * kTokens) & in_page);
+        word[x] = __ldg(reinterpret_cast<const uint32_t*>(codes + row * (D / 2)));
+        scale[x] = __ldg(reinterpret_cast<const unsigned short*>(scales + row * (2 * (D / GROUP))));
+      } else {
+        page[x] = -1;
       }
     }
 #pragma unroll
@@ -303,15 +277,13 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const Kv4Gather
       uint32_t v = word[x];
       if (is_v) {
         // lanes of one row: an even g sends its high half, an odd one its low
-        const bool odd = ((threadIdx.x % kChunks) / (T / 2)) & 1;
         const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? v & 0xffffu : v >> 16, T / 2);
         v = odd ? __byte_perm(other, v, 0x7610) : __byte_perm(v, other, 0x5410);
       }
-      if (pos[x] < 0) continue;
-      *reinterpret_cast<uint4*>(out + (static_cast<size_t>(out0 + pos[x]) * per_token + in_token[x]) * 16) =
-          kv4::values_of<BF16>(v, scale[x]);
+      if (page[x] >= 0)
+        *reinterpret_cast<uint4*>(out + (out0 + pos0 + x * kTokens) * out_row) =
+            kv4::values_of<BF16>(v, scale[x]);
     }
-    forth(far_pos, far_in);
   }
   if (bad) atomicOr(&g_kv4_status, kStatusBadPages);
 }
@@ -336,11 +308,12 @@ struct LaunchAppend {
   template <int D, int GROUP, bool BF16>
   int operator()() const {
     const long long chunks = static_cast<long long>(p.n) * p.pool.hk * (D / 8);
-    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>(chunks) : run<D, GROUP, BF16, 4>(chunks);
+    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>() : run<D, GROUP, BF16, 4>();
   }
   template <int D, int GROUP, bool BF16, int U>
-  int run(long long chunks) const {
-    const dim3 grid(static_cast<unsigned>((chunks + U * kRowThreads - 1) / (U * kRowThreads)), 2);
+  int run() const {
+    constexpr int kTokens = U * kRowThreads / (D / 8);
+    const dim3 grid((p.n + kTokens - 1) / kTokens, p.pool.hk, 2);
     kv4_append_kernel<D, GROUP, BF16, U><<<grid, kRowThreads, 0, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }
@@ -355,15 +328,15 @@ struct LaunchGather {
   template <int D, int GROUP, bool BF16>
   int operator()() const {
     const long long chunks = static_cast<long long>(p.rows) * p.pool.hk * (D / 8);
-    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>(chunks) : run<D, GROUP, BF16, 4>(chunks);
+    return chunks < kRowsWide ? run<D, GROUP, BF16, 1>() : run<D, GROUP, BF16, 4>();
   }
   template <int D, int GROUP, bool BF16, int U>
-  int run(long long chunks) const {
+  int run() const {
     // one sweep of a sequence of the average length
-    long long per_seq = (chunks / p.nseq + U * kRowThreads - 1) / (U * kRowThreads);
-    if (per_seq < 1) per_seq = 1;
-    if (per_seq > 16384) per_seq = 16384;
-    const dim3 grid(static_cast<unsigned>(per_seq), p.nseq, 2);
+    constexpr int kTokens = U * kRowThreads / (D / 8);
+    int sweep = (p.rows / p.nseq + kTokens - 1) / kTokens;
+    sweep = sweep < 1 ? 1 : sweep > 16384 ? 16384 : sweep;
+    const dim3 grid(sweep, p.nseq, 2 * p.pool.hk);
     kv4_gather_kernel<D, GROUP, BF16, U><<<grid, kRowThreads, 0, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }

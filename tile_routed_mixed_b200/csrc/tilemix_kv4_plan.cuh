@@ -17,7 +17,7 @@
 namespace tilemix {
 
 constexpr int kPlanThreads = 512;
-constexpr int kPlanCluster = 8;  // CTAs of a large call
+constexpr int kPlanCluster = 16;  // CTAs of a large call
 
 namespace plan {
 
@@ -46,39 +46,29 @@ __device__ __forceinline__ int count_le(const int* a, int n, int x) {
   return lo;
 }
 
-struct Sums {
-  long long grow, need, back;
-};
-__device__ __forceinline__ Sums operator+(const Sums& a, const Sums& b) {
-  return {a.grow + b.grow, a.need + b.need, a.back + b.back};
-}
-__device__ __forceinline__ Sums shfl_up(const Sums& a, int by) {
-  return {__shfl_up_sync(0xffffffffu, a.grow, by), __shfl_up_sync(0xffffffffu, a.need, by),
-          __shfl_up_sync(0xffffffffu, a.back, by)};
-}
-
-// Exclusive sum over the block's threads; the total in *total.
-__device__ __forceinline__ Sums block_exclusive(const Sums& mine, Sums* total) {
-  __shared__ Sums warp_sum[kPlanThreads / 32];
+// Exclusive sums over the block's threads, and the totals.
+template <class X>
+__device__ __forceinline__ X block_exclusive(X mine, X* total) {
+  __shared__ X warp_sum[kPlanThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Sums inc = mine;
+  X upto = mine;
 #pragma unroll
   for (int by = 1; by < 32; by <<= 1) {
-    const Sums up = shfl_up(inc, by);
-    if (lane >= by) inc = inc + up;
+    const X up = __shfl_up_sync(0xffffffffu, upto, by);
+    if (lane >= by) upto += up;
   }
-  if (lane == 31) warp_sum[warp] = inc;
+  if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  Sums base{0, 0, 0}, all{0, 0, 0};
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    const Sums x = warp_sum[w];
-    if (w < warp) base = base + x;
-    all = all + x;
+  // every warp adds up the warps' sums for itself
+  X all = lane < kPlanThreads / 32 ? warp_sum[lane] : X(0);
+#pragma unroll
+  for (int by = 1; by < 32; by <<= 1) {
+    const X up = __shfl_up_sync(0xffffffffu, all, by);
+    if (lane >= by) all += up;
   }
-  __syncthreads();
-  *total = all;
-  return {base.grow + inc.grow - mine.grow, base.need + inc.need - mine.need,
-          base.back + inc.back - mine.back};
+  *total = __shfl_sync(0xffffffffu, all, 31);
+  const X before = __shfl_sync(0xffffffffu, all, max(warp - 1, 0));
+  return (warp > 0 ? before : X(0)) + upto - mine;
 }
 
 __device__ __forceinline__ int clamp31(long long x) {
@@ -121,53 +111,56 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
   const int per = (p.nseq + kPlanThreads - 1) / kPlanThreads;
   const int s0 = min(p.nseq, tid * per), s1 = min(p.nseq, s0 + per);
   const int free_in = *p.free_count;
-  plan::Sums mine{0, 0, 0};
   bool bad = free_in < 0 || free_in > p.num_pages;
   const long long F = min(max(free_in, 0), p.num_pages);
   const auto pages = [&](long long t) { return static_cast<int>((t + ps1) >> sh); };
+  __shared__ int granted_pages;
+  if (tid == 0) granted_pages = 0;
   // tokens first: whether a sequence fits depends on where its tokens end
+  long long tokens_here = 0;
+  int back_here = 0;  // all returned pages: fewer than nseq * max_pages < 2^31
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     const plan::Row r = plan::row_of(p.seq_len[s], __ldg(p.new_len + s), top);
     bad |= r.bad;
-    mine.grow += r.grow;
-    mine.back += pages(r.len) - pages(r.len - r.drop);
+    tokens_here += r.grow;
+    back_here += pages(r.len) - pages(r.len - r.drop);
     len_s[s] = r.len;
   }
-  plan::Sums total;
-  plan::Sums before = plan::block_exclusive(mine, &total);
-  const long long R = total.back;  // fewer than nseq * max_pages < 2^31
-  long long end = before.grow, back = before.back;
+  long long tokens;
+  int returned;
+  long long end = plan::block_exclusive(tokens_here, &tokens);
+  int back = plan::block_exclusive(back_here, &returned);
+  long long need_here = 0;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
-    const int n = __ldg(p.new_len + s), len = len_s[s];
-    const int grow = n > 0 ? n : 0;
-    const int drop = plan::row_of(len, n, top).drop;
-    const long long after = static_cast<long long>(len) + grow;
-    end += grow;
-    back += pages(len) - pages(len - drop);
+    const plan::Row r = plan::row_of(len_s[s], __ldg(p.new_len + s), top);
+    const long long after = static_cast<long long>(r.len) + r.grow;
+    end += r.grow;
+    back += pages(r.len) - pages(r.len - r.drop);
     const bool fits = end <= p.max_tokens && after <= top;
-    const int need = fits ? pages(after) - pages(len) : 0;
-    mine.need += need;
+    const int need = fits ? pages(after) - pages(r.len) : 0;
+    need_here += need;
     end_s[s] = plan::clamp31(end);
-    back_s[s] = plan::clamp31(back);
+    back_s[s] = back;
     need_s[s] = need;
     flag_s[s] = fits;
   }
-  plan::Sums total2;
-  plan::Sums before2 = plan::block_exclusive({0, mine.need, 0}, &total2);
-  const long long have = F + R;
-  long long cum = before2.need, used = 0;
+  long long needed;
+  long long cum = plan::block_exclusive(need_here, &needed);
+  const long long R = returned, have = F + R;
+#pragma unroll 1
   for (int s = s0; s < s1; ++s) {
     const int need = need_s[s];
     cum += need;
     const bool ok = __ldg(p.new_len + s) <= 0 || (flag_s[s] && (need == 0 || cum <= have));
-    if (ok) used += need;
+    // pages granted are a prefix of those needed
+    if (ok && need > 0) atomicMax(&granted_pages, static_cast<int>(cum));
     need_s[s] = plan::clamp31(cum);
     flag_s[s] = ok;
   }
-  plan::Sums total3;
-  plan::block_exclusive({0, used, 0}, &total3);
-  used = total3.need;  // granted pages: a prefix of the needed ones
   __syncthreads();
+  const long long used = granted_pages;
   if (clustered) plan::cluster_sync();  // every CTA has read the lengths and the stack's height
 
   // returned pages onto the stack
@@ -259,6 +252,10 @@ int launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
   cudaLaunchAttribute attr{};
   // one CTA covers 2,048 slots in one sweep
   const int ctas = p.max_tokens > 4 * kPlanThreads ? kPlanCluster : 1;
+  if (ctas > 8 &&
+      (e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) !=
+          cudaSuccess)
+    return static_cast<int>(e);
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.dynamicSmemBytes = smem;

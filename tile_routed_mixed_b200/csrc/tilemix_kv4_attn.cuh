@@ -198,6 +198,7 @@ __device__ __forceinline__ Unit unit_after(const Kv4AttnParams& p, Unit x) {
 struct Cut {
   long long total, each;  // all tiles; total / ctas
   int ctas, rest;         // total % ctas
+  long long a, b;         // this CTA's tiles: [a, b)
   __device__ __forceinline__ long long begin(int c) const {  // floor(c * total / ctas)
     return each * c + static_cast<unsigned>(c * rest) / static_cast<unsigned>(ctas);
   }
@@ -220,45 +221,37 @@ struct Part {
   float* at;        // nullptr: none
 };
 
-// One column's four channels from n states: at(i) is state i.  The D / 4 lanes
-// of a column take the states' weights together, one each, and then add up the
-// states in order.
-template <int D, int NB, class At>
-__device__ __forceinline__ float4 combine(int n, int col, int ch, At at, float* ref, float* sum) {
-  constexpr int kCols = 8 * NB, kLanes = D / 4;
-  const int mine = ch / 4, first = (threadIdx.x & 31) - mine;  // of the column's lanes
-  const unsigned who = kLanes == 32 ? 0xffffffffu : 0xffffu << first;
-  float top = -INFINITY;
-#pragma unroll 1
-  for (int i = mine; i < n; i += kLanes) top = fmaxf(top, at(i)[kCols * D + col]);
-#pragma unroll 1
-  for (int by = kLanes / 2; by > 0; by >>= 1) top = fmaxf(top, __shfl_xor_sync(who, top, by));
-  const float to = top == -INFINITY ? 0.f : top;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
-#pragma unroll 1
-  for (int base = 0; base < n; base += kLanes) {
-    const int i = base + mine, m = min(n - base, kLanes);
-    float w = 0.f, li = 0.f;
-    if (i < n) {
-      w = ptx::ex2(at(i)[kCols * D + col] - to);
-      li = at(i)[kCols * (D + 1) + col];
-    }
-#pragma unroll 4
-    for (int k = 0; k < m; ++k) {
-      const float4 y = *reinterpret_cast<const float4*>(at(base + k) + col * D + ch);
-      const float wk = __shfl_sync(who, w, first + k);
-      l = fmaf(wk, __shfl_sync(who, li, first + k), l);
-      acc.x = fmaf(wk, y.x, acc.x);
-      acc.y = fmaf(wk, y.y, acc.y);
-      acc.z = fmaf(wk, y.z, acc.z);
-      acc.w = fmaf(wk, y.w, acc.w);
-    }
-  }
-  *ref = top;
-  *sum = l;
-  return acc;
+// Counts an arrival (up to `last`, then from 0 again); what came before it is seen
+// by those who arrive later.
+__device__ __forceinline__ int arrive(unsigned* counter, int last) {
+  unsigned was;
+  asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;"
+               : "=r"(was)
+               : "l"(counter), "r"(last)
+               : "memory");
+  return static_cast<int>(was);
 }
+
+// Four channels of a column while states are added up, in order.
+struct Fold {
+  float4 acc;
+  float ref, sum;
+  __device__ __forceinline__ void clear() {
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    ref = -INFINITY;
+    sum = 0.f;
+  }
+  __device__ __forceinline__ void add(const float4& y, float r, float l) {
+    const float to = fmaxf(ref, r), at = to == -INFINITY ? 0.f : to;
+    const float wa = ptx::ex2(ref - at), wb = ptx::ex2(r - at);
+    ref = to;
+    sum = fmaf(sum, wa, l * wb);
+    acc.x = fmaf(acc.x, wa, y.x * wb);
+    acc.y = fmaf(acc.y, wa, y.y * wb);
+    acc.z = fmaf(acc.z, wa, y.z * wb);
+    acc.w = fmaf(acc.w, wa, y.w * wb);
+  }
+};
 
 // Four channels of a finished column to O, and its LSE.
 template <int D, int NB, bool BF16>
@@ -290,12 +283,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   static_assert(kStages < 8, "a tile ahead may be a unit ahead");
   __shared__ kv4::Part parts[2 * kWarps];
   __shared__ const float* state[2 * kWarps];  // the partial states there are, in order
-  __shared__ int state_of[2 * kWarps];        // ... each one's place in parts
-  __shared__ int run_begin[2 * kWarps + 1], run_count;
-  __shared__ kv4::Cut cut_s;     // for the end: kept out of the registers meanwhile
-  __shared__ long long range_s[2];  // a and b, likewise
-  __shared__ int holders[2][2];  // first and last CTA of a shared unit
-  __shared__ int last_here[2];
+  __shared__ kv4::Cut cuts[kWarps];  // each warp's: kept out of the registers meanwhile
+  // first and last CTA of the unit that the CTA's first, and its last, tile is of
+  __shared__ int holders[2][2];
+  __shared__ int state_of[2 * kWarps];
+  __shared__ int last_here[2];  // states to combine, if this CTA is the last to arrive
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
@@ -341,14 +333,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       cut.each = cut.total / cut.ctas;
     }
     cut.rest = static_cast<int>(cut.total - cut.each * cut.ctas);
-    const long long a = cut.begin(blockIdx.x), b = cut.begin(blockIdx.x + 1);
-    wa = a + (b - a) * warp / kWarps;
-    wb = a + (b - a) * (warp + 1) / kWarps;
-    if (tid == 0) {
-      cut_s = cut;
-      range_s[0] = a;
-      range_s[1] = b;
-    }
+    cut.a = cut.begin(blockIdx.x);
+    cut.b = cut.begin(blockIdx.x + 1);
+    wa = cut.a + (cut.b - cut.a) * warp / kWarps;
+    wb = cut.a + (cut.b - cut.a) * (warp + 1) / kWarps;
+    if (lane == 0) cuts[warp] = cut;
     // the sequence that holds tile wa: the lane's share, then one by one
     const uint32_t from = __ballot_sync(0xffffffffu, upto - mine <= wa);
     const int at = 31 - __clz(from);
@@ -493,6 +482,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       const int n = min(left, cur.w.tiles - t0);
       const bool whole = t0 == 0 && n == cur.w.tiles;
       const bool head = !whole && n < left;  // more tiles of this warp follow
+      // who else holds the CTA's first and last unit, found while loads are on the way
+      if (lane == 0) {
+        const kv4::Cut& cut = cuts[warp];
+        for (int i = 0; i < 2; ++i)
+          if (i == 0 ? wa == cut.a && units_done == 0 : wb == cut.b && n == left) {
+            holders[i][0] = cut.holder(unit_first);
+            holders[i][1] = cut.holder(unit_first + cur.w.tiles - 1);
+          }
+      }
       uint32_t qf[NB][kT][4];
       float cs[NB][2];  // scale of a column's scores, log2 units
       int lim[NB][2];  // keys that each column sees
@@ -791,89 +789,114 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   }
 
   // ---- the CTA's partial states; what other CTAs share goes on ----
-  // States lie in the order of the tiles, so those of one unit are neighbours:
-  // a run.  Every run at once, a thread to a column's four channels; each unit
-  // that lies within the CTA is finished, the first and the last may be shared.
+  // States lie in the order of the tiles, so those of one unit are neighbours: a
+  // run.  A thread has a column's four channels and goes through all states once,
+  // four loads ahead; where a run ends, the unit is finished or, if other CTAs
+  // have tiles of it too (the first and the last unit may be such), its state
+  // is passed on.
   __syncthreads();
   constexpr int kItems = kCols * (D / 4);
   constexpr size_t kPart = kv4::kPartFloats<D, NB>;
-  if (warp == 0) {
+  uint32_t here, starts;  // states there are; those that begin a run
+  {
     const bool present = lane < 2 * kWarps && parts[lane].at != nullptr;
-    const uint32_t here = __ballot_sync(0xffffffffu, present);
+    here = __ballot_sync(0xffffffffu, present);
     const uint32_t before = here & ((1u << lane) - 1u);
-    const bool begins =
-        present && (before == 0 || parts[31 - __clz(before)].first != parts[lane].first);
-    const uint32_t starts = __ballot_sync(0xffffffffu, begins);
-    if (present) {
+    starts = __ballot_sync(
+        0xffffffffu, present && (before == 0 || parts[31 - __clz(before)].first != parts[lane].first));
+    const uint32_t after = here & (lane == 31 ? 0u : 0xffffffffu << (lane + 1));
+    if (present) {  // (every warp writes the same)
       state[__popc(before)] = parts[lane].at;
-      state_of[__popc(before)] = lane;
+      // its place in parts, and whether it ends its run
+      state_of[__popc(before)] = lane | (after == 0 || (starts >> (__ffs(after) - 1) & 1u) ? 64 : 0);
     }
-    if (begins) run_begin[__popc(starts & ((1u << lane) - 1u))] = __popc(before);
-    if (lane == 0) {
-      run_count = __popc(starts);
-      run_begin[__popc(starts)] = __popc(here);
-    }
+    __syncwarp();
   }
-  __syncthreads();
-  const int runs = run_count;
-  const long long a = range_s[0], b = range_s[1];
-  if (runs == 0) return;
+  if (here == 0) return;
+  const long long a = cuts[warp].a, b = cuts[warp].b;
   const auto shared_unit = [&](const kv4::Part& u) {
     return u.first < a || u.first + u.unit.w.tiles > b;
   };
-  // First each run; then, of the first and the last unit (0 and 1 below) those
-  // that are shared, if this CTA is the last of theirs to arrive: all of the
-  // unit's CTAs' states, in order.
-  const int ends[2] = {state_of[0], state_of[run_begin[runs - 1]]};
+  const int ends[2] = {__ffs(starts) - 1, 31 - __clz(starts)};
+  int n = __popc(here), n0 = 0;
   bool again = false;
+  const int* span0 = nullptr;
+  const int* span1 = nullptr;
 #pragma unroll 1
-  for (int items = runs * kItems;; items = 2 * kItems) {
+  for (;;) {
+    // first this CTA's states; then, of the two shared units (if this CTA is the
+    // last of theirs to arrive), n0 and n - n0 CTAs' states
+    const auto at = [&](int k) -> const float* {
+      if (!again) return state[k];
+      const int* const span = k < n0 ? span0 : span1;
+      const int c = k < n0 ? k : k - n0;
+      return p.parts + static_cast<size_t>(2 * (span[0] + c) + (c == 0 ? 1 : 0)) * kPart;
+    };
 #pragma unroll 1
-    for (int x = tid; x < items; x += kThreads) {
-      const int i = x / kItems, col = x % kItems / (D / 4), ch = 4 * (x % (D / 4));
-      if (again && !last_here[i]) continue;
-      const kv4::Part& u = parts[again ? (i == 0 ? ends[0] : ends[1]) : state_of[run_begin[i]]];
-      const int c0 = again ? holders[i][0] : 0;
-      const int n = again ? holders[i][1] - c0 + 1 : run_begin[i + 1] - run_begin[i];
-      const float* const* states = state + (again ? 0 : run_begin[i]);
-      const float* cta_states = p.parts + static_cast<size_t>(2 * c0) * kPart;
-      float ref, sum;
-      const float4 acc = kv4::combine<D, NB>(
-          n, col, ch,
-          [&](int k) { return again ? cta_states + (k == 0 ? 1 : 2 * k) * kPart : states[k]; }, &ref, &sum);
-      if (again || !shared_unit(u)) {
-        kv4::store_column<D, NB, BF16>(p, u.unit, col, ch, acc, ref, sum);
-      } else {
-        // to this CTA's first place (the unit began before its tiles) or second
-        float* out = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart;
-        *reinterpret_cast<float4*>(out + col * D + ch) = acc;
-        if (ch == 0) {
-          out[kCols * D + col] = ref;
-          out[kCols * (D + 1) + col] = sum;
+    for (int x = tid; x < kItems; x += kThreads) {
+      const int col = x / (D / 4), ch = 4 * (x % (D / 4));
+      float4 y[4];
+      float r[4], l[4];
+      const auto fetch = [&](int k, int slot) {
+        if (k < n) {
+          const float* from = at(k);
+          y[slot] = *reinterpret_cast<const float4*>(from + col * D + ch);
+          r[slot] = from[kCols * D + col];
+          l[slot] = from[kCols * (D + 1) + col];
+        }
+      };
+#pragma unroll
+      for (int j = 0; j < 4; ++j) fetch(j, j);
+      kv4::Fold f;
+      f.clear();
+#pragma unroll 1
+      for (int k0 = 0; k0 < n; k0 += 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = k0 + j;
+          if (k >= n) break;
+          f.add(y[j], r[j], l[j]);
+          fetch(k + 4, j);
+          const int of = again ? (k + 1 == n0 ? ends[0] | 64 : k + 1 == n ? ends[1] | 64 : 0) : state_of[k];
+          if (of & 64) {
+            const kv4::Part& u = parts[of & 63];
+            if (again || !shared_unit(u)) {
+              kv4::store_column<D, NB, BF16>(p, u.unit, col, ch, f.acc, f.ref, f.sum);
+            } else {
+              // to this CTA's first place (the unit began before its tiles) or second
+              float* out = p.parts + (2 * static_cast<size_t>(blockIdx.x) + (u.first < a ? 0 : 1)) * kPart;
+              *reinterpret_cast<float4*>(out + col * D + ch) = f.acc;
+              if (ch == 0) {
+                out[kCols * D + col] = f.ref;
+                out[kCols * (D + 1) + col] = f.sum;
+              }
+            }
+            f.clear();
+          }
         }
       }
     }
     if (again) return;
     again = true;
     const bool shares0 = shared_unit(parts[ends[0]]);
-    const bool shares1 = runs > 1 && shared_unit(parts[ends[1]]);
+    const bool shares1 = ends[1] != ends[0] && shared_unit(parts[ends[1]]);
     if (!shares0 && !shares1) return;
+    span0 = holders[parts[ends[0]].first < a ? 0 : 1];
+    span1 = holders[1];
     __syncthreads();
     if (lane == 0 && warp < 2) {
       int last = 0;
       if (warp == 0 ? shares0 : shares1) {
-        const kv4::Part& u = parts[warp == 0 ? ends[0] : ends[1]];
-        const int c0 = cut_s.holder(u.first), c1 = cut_s.holder(u.first + u.unit.w.tiles - 1);
-        holders[warp][0] = c0;
-        holders[warp][1] = c1;
-        __threadfence();
+        const int* const span = warp == 0 ? span0 : span1;
+        const int others = span[1] - span[0];
         // wraps to zero with the last arrival, so the array is zero again
-        last = atomicInc(p.sync + c0, c1 - c0) == static_cast<unsigned>(c1 - c0);
-        __threadfence();
+        last = kv4::arrive(p.sync + span[0], others) == others ? others + 1 : 0;
       }
       last_here[warp] = last;
     }
     __syncthreads();
+    n0 = last_here[0];
+    n = n0 + last_here[1];
   }
 }
 

@@ -48,12 +48,14 @@ namespace tilemix {
 
 constexpr int kAttnKeys = 32;  // keys of a tile
 
-// Warps of a CTA (one CTA per SM), by column blocks: a warp's state and
-// operands fit 128 registers with 8 columns, 255 with 16.
+// Warps of a CTA (one CTA per SM), by column blocks.  Eight columns fit 168
+// registers a thread; with 16 warps of 128 the largest batch is as fast (262 us,
+// 259 with 12, 283 with 8), but a single short sequence has more states to combine
+// (12.6 us, 11.5, 10.8).  Sixteen columns need 255.
 template <int NB>
-constexpr int kAttnWarps = NB == 1 ? 16 : 8;
+constexpr int kAttnWarps = NB == 1 ? 12 : 8;
 constexpr int kAttnMaxCtas = 160;  // at least one per SM (148 on a B200)
-constexpr int kAttnMinTiles = 16;  // tiles a CTA takes at least, while there are any
+constexpr int kAttnMinTiles = 8;  // tiles a CTA takes at least, while there are any
 
 template <int D, int GROUP, int NB>
 struct AttnTile {
@@ -62,7 +64,6 @@ struct AttnTile {
   static constexpr int kCodes = kAttnKeys * D / 2;      // bytes of K's (and V's) codes
   static constexpr int kScales = kAttnKeys * 2 * kNg;   // ... and scales
   static constexpr int kBytes = 2 * kCodes + 2 * kScales;
-  static constexpr int kRowBytes = D + 4 * kNg;         // of one key, K and V
   static constexpr int kOffV = kCodes;
   static constexpr int kOffKs = 2 * kCodes;
   static constexpr int kOffVs = 2 * kCodes + kScales;
@@ -302,12 +303,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     const int per = (p.nseq + 31) / 32;
     const int s0 = min(p.nseq, lane * per), s1 = min(p.nseq, s0 + per);
     long long mine = 0;
-    int units = 0;
+    int units = 0, shortest = 0x7fffffff, longest = 0;
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
       const kv4::SeqWork w = kv4::seq_work<NB>(p, s);
       mine += kv4::seq_tiles(p, w);
       units = min(units + p.pool.hk * w.blocks, 1 << 20);  // all that matters: fewer than CTAs?
+      if (w.blocks > 0) shortest = min(shortest, w.tiles), longest = max(longest, w.tiles);
     }
     long long upto = mine;
 #pragma unroll
@@ -317,14 +319,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     }
     units = __reduce_add_sync(0xffffffffu, units);
     cut.total = __shfl_sync(0xffffffffu, upto, 31);
-    // CTAs that take part.  With fewer units than CTAs each unit gets the same
-    // number of them (units of one length are then cut at their own ends, and
-    // none shares a CTA); otherwise the ranges go where they fall.
-    cut.ctas = gridDim.x;
-    if (units < cut.ctas) {
-      const int some = static_cast<int>(min(cut.total, 1LL << 30));
-      units = max(units, 1);
-      cut.ctas = units * max(1, min(some / (units * kAttnMinTiles), cut.ctas / units));
+    // CTAs that take part: all, while each gets a few tiles.  Units of one length
+    // are better cut at their own ends, the same number of CTAs for each, if that
+    // leaves no more than a seventh of the CTAs idle: no CTA then has parts of two
+    // units (8 x 4096, 24/8 heads: 18.6 us on 128 CTAs, 20.3 on 148; twelve ragged
+    // sequences of 35 columns: 53 us on all, 76 on a number for each unit).
+    const int some = static_cast<int>(min(cut.total, 1LL << 30));
+    cut.ctas = min(static_cast<int>(gridDim.x), max(units, some / kAttnMinTiles));
+    if (units <= cut.ctas && units > 0 &&
+        __reduce_min_sync(0xffffffffu, shortest) == __reduce_max_sync(0xffffffffu, longest)) {
+      const int aligned = units * max(1, min(some / (units * kAttnMinTiles), cut.ctas / units));
+      if (aligned * 7 >= cut.ctas * 6) cut.ctas = aligned;
     }
     if (static_cast<int>(blockIdx.x) >= cut.ctas || cut.total == 0) return;
     if (cut.total <= 0x7fffffffLL) {

@@ -647,7 +647,9 @@ int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
  *   magnitude, each probability times its V scale is rounded once to 11 bits),
  *   O rounded once to the cache's type.
  * A query with no position to attend to gets O = 0 and an LSE of -infinity.  A
- * sequence with no queries reads nothing.  Rows of q and o at and behind
+ * sequence with no queries reads nothing.  A table entry that names no page is
+ * reported by tilemix_get_error() as INVALID_ARG; what its sequence gets is then
+ * meaningless.  Rows of q and o at and behind
  * token_start[nseq] are not touched.  One launch; results do not depend on
  * timing (partial results are combined in a fixed order).
  * Queries are taken in blocks of 8 (or 16, if max_new * hq / hk > 8) columns, a
@@ -667,7 +669,7 @@ typedef struct tilemix_kv4_attn_args {
   int total_q;                /* rows of q and o, >= 0 */
   int max_new;                /* most queries of a sequence, >= 1: picks the column block,
                                  a smaller value than the true one costs only time */
-  int max_seqlen;             /* longest sequence, >= 1: sizes the grid, likewise */
+  int max_seqlen;             /* longest sequence, >= 1: bounds the grid, likewise */
   int max_pages;              /* >= 1 */
   int hq;                     /* hq % hk == 0 */
   float softmax_scale;        /* 0 => 1 / sqrt(d) */

@@ -573,3 +573,95 @@ def test_workspace_size_is_checked():
             tm.tilemix_kv4_attn(b)
         assert e.value.status == tm.ERR_WORKSPACE
     assert ctypes.sizeof(a) > 0
+
+
+def test_call_site_refusals():
+    """Wrong types, shapes, layouts and counts are refused before anything is
+    enqueued, and leave the cache usable."""
+    import tile_routed_mixed_b200 as tm
+    rng = np.random.default_rng(24)
+    pool = kc.Pool(rng, [40, 3], 2, 64, 32, 16, "fp16")
+    cache = pool.cache()
+    h = lambda *s: torch.zeros(s, dtype=torch.float16, device="cuda")
+    bad = [
+        lambda: cache.plan(_i32([1, 1, 1]), max_tokens=3),                          # more than max_seqs
+        lambda: cache.plan(_i32([1, 1])),                                           # no slots given
+        lambda: cache.plan(_i32([1, 1]).long(), max_tokens=2),
+        lambda: cache.plan(_i32([1, 1], "cpu"), max_tokens=2),
+        lambda: cache.plan(_i32([1, 0, 1, 0])[::2], max_tokens=2),
+        lambda: cache.plan(_i32([1, 1]), max_tokens=3, out=cache.new_plan(2)),
+        lambda: cache.plan(_i32([1]), out=cache.new_plan(2)),
+        lambda: cache.append(h(2, 2, 64), h(2, 2, 64).bfloat16(), _i32([0, 1])),
+        lambda: cache.append(h(1, 2, 64), h(2, 2, 64), _i32([0, 1])),               # fewer rows than slots
+        lambda: cache.append(h(2, 2, 128)[..., ::2], h(2, 2, 64), _i32([0, 1])),
+        lambda: cache.append(h(2, 64, 2).transpose(1, 2), h(2, 2, 64), _i32([0, 1])),
+        lambda: cache.append(h(2, 2, 64), h(2, 2, 64), _i32([0, 1]).long()),
+        lambda: cache.gather(_i32([0, 0, 0]), 5),
+        lambda: cache.gather(_i32([0, 40]), 43, out=(h(43, 2, 64), h(42, 2, 64))),
+        lambda: cache.attend(h(2, 3, 64), 40),                                      # 3 heads over 2
+        lambda: cache.attend(h(2, 4, 32), 40),
+        lambda: cache.attend(h(3, 4, 64), 40),                                      # more rows than sequences
+        lambda: cache.attend(h(2, 4, 64).float(), 40),
+        lambda: cache.attend(h(2, 4, 64), 40, out=h(2, 4, 64).bfloat16()),
+        lambda: cache.attend(h(2, 4, 64), 40, lse=torch.zeros((2, 4), device="cuda")),
+        lambda: cache.attend(h(2, 4, 64), 40, token_start=_i32([0, 1, 2, 2])),
+        lambda: tm.TileMixKV4Cache(4, 16, 1, 64, 2, 2, group=128),
+        lambda: tm.TileMixKV4Cache(4, 16, 1, 64, 2, 2, dtype=torch.float32),
+        lambda: tm.TileMixKV4Cache(4, 16, 1, 64, 2, 2, device="cpu"),
+        lambda: tm.TileMixKV4Cache(0, 16, 1, 64, 2, 2),
+        lambda: tm.TileMixKV4Cache(4, 16, 1, 64, 2, 2, pool=pool.tensors()),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail("case %d was taken" % i)
+    for f in (lambda: cache.attend(h(2, 4, 64), 40, softmax_scale=float("nan")),
+              lambda: cache.attend(h(2, 4, 64), 40, max_new=0),
+              lambda: cache.attend(h(2, 4, 64), 0)):
+        with pytest.raises(tm.TileMixError):
+            f()
+    _attend(pool, [1, 2], 4, cache=cache)
+
+
+def test_two_threads_on_one_cache():
+    """Two host threads with a stream each, calling one object."""
+    import threading
+    rng = np.random.default_rng(25)
+    pool = kc.Pool(rng, [900, 70], 2, 64, 64, 32, "bf16")
+    cache = pool.cache()
+    q = [kc.draw(rng, (2, 4 * (i + 1), 64), "bf16") for i in range(2)]
+    qd = [kc.to_device(x, "bf16") for x in q]
+    outs = [None, None]
+    torch.cuda.synchronize()
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(200):
+            outs[i] = cache.attend(qd[i], 900, stream=s)
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        kc.check_attend(kc.to_numpy(outs[i]), None, q[i], pool, [900, 70], [0, 1, 2], 4 * (i + 1))
+
+
+def test_bounds_that_are_too_small_cost_only_time():
+    rng = np.random.default_rng(26)
+    pool = kc.Pool(rng, [700, 300], 2, 64, 32, 16, "fp16")
+    cache = pool.cache()
+    q = kc.draw(rng, (5, 6, 64), "fp16")
+    o = cache.attend(kc.to_device(q, "fp16"), 1, token_start=_i32([0, 3, 5]), max_new=1)
+    kc.check_attend(kc.to_numpy(o), None, q, pool, [700, 300], [0, 3, 5], 6)
+
+
+def test_rows_of_one_page_in_many_sequences():
+    """Sequences that share their first pages (a common prefix) read the same rows."""
+    rng = np.random.default_rng(27)
+    pool = kc.Pool(rng, [64, 50, 33], 1, 128, 64, 16, "bf16")
+    pool.table[1, :2] = pool.table[0, :2]
+    pool.table[2, :2] = pool.table[0, :2]
+    _attend(pool, [1, 1, 2], 2)

@@ -94,7 +94,7 @@ struct AttnLayout {
 AttnLayout attn_layout(const tilemix_kv4_attn_args* a) {
   AttnLayout w;
   const long long columns = static_cast<long long>(a->max_new) * (a->hq / a->cache.hk);
-  w.shape = tilemix::kv4_attn_shape(current_sms(), columns);
+  w.shape = tilemix::kv4_attn_shape(current_sms(), columns, a->nseq, a->cache.hk, a->max_seqlen);
   const size_t state = static_cast<size_t>(w.shape.cols) * (a->cache.d + 2) * sizeof(float);
   w.heads = 0;
   w.parts = state * w.shape.ctas * w.shape.warps;

@@ -73,11 +73,12 @@ struct Kv4Format {
 int launch_page_plan(const PagePlanParams& p, cudaStream_t stream);
 int launch_kv4_append(const Kv4AppendParams& p, const Kv4Format& f, cudaStream_t stream);
 int launch_kv4_gather(const Kv4GatherParams& p, const Kv4Format& f, cudaStream_t stream);
-// CTAs of an attention launch, warps of each, and columns of its blocks.
+// Attention launches: the most CTAs on this device (one per SM; sizes the
+// workspace), those of this launch, warps of each, and columns of a block.
 struct Kv4AttnShape {
-  int ctas, warps, cols;
+  int ctas, grid, warps, cols;
 };
-Kv4AttnShape kv4_attn_shape(int sms, long long columns);
+Kv4AttnShape kv4_attn_shape(int sms, long long columns, long long nseq, int hk, long long keys);
 int launch_kv4_attn(const Kv4AttnParams& p, const Kv4Format& f, const Kv4AttnShape& shape,
                     cudaStream_t stream);
 int kv4_read_and_clear_status(unsigned int* status);

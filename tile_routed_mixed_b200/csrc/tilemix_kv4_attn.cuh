@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // ---- a unit: its queries ----
       const kv4::Unit& cur = ahead[units_done & 7];
       const int t0 = units_done == 0 ? t_first : 0, keys = cur.keys;
-      const int n = min(left, cur.w.tiles - t0);
+      const int n = max(1, min(left, cur.w.tiles - t0));  // (1: always onwards)
       const bool whole = t0 == 0 && n == cur.w.tiles;
       const bool head = !whole && n < left;  // more tiles of this warp follow
       // who else holds the CTA's first and last unit, found while loads are on the way
@@ -905,9 +905,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   }
 }
 
-Kv4AttnShape kv4_attn_shape(int sms, long long columns) {
-  const int ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
-  return columns > 8 ? Kv4AttnShape{ctas, kAttnWarps<2>, 16} : Kv4AttnShape{ctas, kAttnWarps<1>, 8};
+Kv4AttnShape kv4_attn_shape(int sms, long long columns, long long nseq, int hk, long long keys) {
+  Kv4AttnShape s;
+  s.ctas = sms < kAttnMaxCtas ? sms : kAttnMaxCtas;
+  s.cols = columns > 8 ? 16 : 8;
+  s.warps = columns > 8 ? kAttnWarps<2> : kAttnWarps<1>;
+  // CTAs that the longest batch of these bounds could use
+  const long long units = nseq * hk * ((columns + s.cols - 1) / s.cols);
+  const long long by_tiles = units * ((keys + kAttnKeys - 1) / kAttnKeys) / kAttnMinTiles;
+  const long long most = units > by_tiles ? units : by_tiles;
+  s.grid = most < 1 ? 1 : most < s.ctas ? static_cast<int>(most) : s.ctas;
+  return s;
 }
 
 struct LaunchAttn {
@@ -927,7 +935,7 @@ struct LaunchAttn {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return static_cast<int>(e);
-    kernel<<<shape.ctas, 32 * kWarps, smem, stream>>>(p);
+    kernel<<<shape.grid, 32 * kWarps, smem, stream>>>(p);
     return static_cast<int>(cudaGetLastError());
   }
 };

@@ -87,21 +87,23 @@ class Pool:
 def attend_bounds(o, lse, mag, reach, dtype, vmax, keys):
     """Largest |error| of O and of the LSE that the arithmetic allows.
 
-    Scores: at most 8 accumulating products per group and a correction, each
-    within 2^-22 of the sum of magnitudes (fp32 sums of the products, which may
-    be truncated), sum |q' u| <= 15 / 7 of sum |q| times the largest |k| (3, as
-    a subnormal scale may leave a smaller largest code), so 8 * 2^-22 * 3 reach
-    and as much again for the correction, its sum and the two products by
+    Scores: at most 8 accumulating products per group, each within 2^-22 of the
+    sum of magnitudes (fp32 sums of the products, which may be truncated), which
+    the largest |k| over its code bounds by 3 reach (a subnormal scale may leave
+    a smaller largest code), so 8 * 2^-22 * 3 reach; as much again covers q's
+    rounding to its scaled fp16, the sum over groups and the two products by
     scales.  A probability is off by that factor (in numerator and sum: twice),
     by ex2's 2^-22 and by its rounding times the scale to 11 bits, 2^-11; below
     fp16's normal range by 2^-25 of a unit of sigma / 32 each, seven times for
-    the code.  The products with V hold a code as code + 8: each of the
-    keys / 16 accumulating steps (and the one that takes 8 sum(P) off) is within
-    2^-21 of the sums' magnitude, at most (16 + 8) sum(P s_v).  O's own rounding is half a step; subnormal results half a unit
-    of 2^-24 (fp16)."""
+    the code.  The products with V take the codes as they are, |code| <= 7 with
+    vmax the largest scale: each of the keys / 16 accumulating steps, and two
+    where partial states are joined, is within 2^-21 of the sums' magnitude, at
+    most 7 sum(P s_v), 8 with P s_v's rounding.  O's own rounding is half a step;
+    subnormal results half a unit of 2^-24 (fp16)."""
     ds = 16 * 2.0 ** -22 * 3 * reach
     rel = 2.0 ** -11 + 2 * ds + 2.0 ** -18
-    tiny = keys * 7 * 2.0 ** -30 * vmax + (keys / 16 + 2) * 2.0 ** -21 * 24 * vmax + (2.0 ** -25 if dtype == "fp16" else 0.0)
+    tiny = keys * 7 * 2.0 ** -30 * vmax + (keys / 16 + 2) * 2.0 ** -21 * 8 * vmax
+    tiny += 2.0 ** -25 if dtype == "fp16" else 0.0
     do = EPS[dtype] * np.abs(o) + (1 + EPS[dtype]) * rel[..., None] * mag + tiny
     dl = ds + 2.0 ** -18 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0.0))
     return do, dl

@@ -7,12 +7,13 @@
 // the split over a long axis and the balance of a ragged batch are the same
 // thing.  A warp works alone: it streams its tiles through a ring of its own
 // in shared memory (cp.async), with its own running maximum, sum and output,
-// and meets the other warps of its CTA only once, at the end.
+// and meets the other warps of its CTA only once, at the end, where a thread
+// goes through all of the CTA's partial states; units that CTAs share are
+// finished by the last of theirs to arrive.  No warp waits for another CTA.
 //
-// Products.  The step reads each cached byte once and is bound by HBM as long
-// as a tile's arithmetic stays under its transfer time, about 180 cycles of an
-// SM for the 4.2 KB of a tile.  What has to be short is the way from 4 bits to
-// an operand of the matrix product:
+// Products.  The step reads each cached byte once; HBM brings the 4.2 to 4.6 KB
+// of a tile to an SM in about 190 cycles.  What has to be short is the way from
+// 4 bits to an operand of the matrix product:
 //   - codes are stored as u = code + 8: a nibble in the low bits of an fp16
 //     whose exponent field is that of 1024 makes it 1024 + u (one three-input
 //     logic operation), and one packed addition leaves the code itself, an exact
@@ -23,14 +24,18 @@
 //     off sums that are large against the result: over 16,000 keys a warp, with
 //     the truncation in the products' sums, that cost a factor of three in O's
 //     error; and at five instructions products are aligned by the subnormals'
-//     exponent and lose six bits more.)
-//   - keys are the rows (M = 16) of both products, queries the 8 columns, so
-//     that no row is padding: S^T = K Q^T, and O^T = V^T P^T;
+//     exponent and lose six bits more.  A nibble in a byte is also the e4m3
+//     number u 2^-9, at three instructions, but mma.sync on e4m3 is carried out
+//     as conversions and fp16 products here: 380 us for 274, largest batch.)
+//   - keys are the rows (M = 16) of the scores' product and channels those of
+//     P V: S^T = K Q^T, O^T = V^T P^T, so no row is padding and the query columns
+//     are the narrow side (N = 8).  (Queries as rows of S would save P's
+//     transposition, but needs registers for zero rows: 390 us for 256.)
 // Q is scaled per column by a power of two, so its largest magnitude is near
 // 2^14 and every channel keeps at least 11 bits (fp16 has 5 of exponent,
 // bf16 has 8) down to 2^-28 of it.  K's scales multiply the scores, V's the
-// probabilities: P s_v is what is rounded to fp16.  A column's probabilities are
-// 2^(score - r) with r = the largest score + log2 of the largest V scale (its
+// probabilities: P s_v is what is rounded to fp16 (11 bits).  A column's
+// probabilities are 2^(score - r) with r = the largest score + log2 of the largest V scale (its
 // power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
 // a score passes the old largest by 8 or a scale doubles: P s_v stays below
 // 2^14, and fp32 holds the sums.  r cancels between O and the sum.
@@ -41,6 +46,17 @@
 // block of 16 is key r ^ ((r >> 1) & 1): the four keys that a quarter of the
 // lanes reads from V, and the two that eight lanes read from K, then fall
 // into different banks (with V's 16-byte chunks exchanged by bit 2 of the key).
+//
+// Measured (B200; from a graph of calls over three caches in turn): 64 ragged
+// sequences of up to 32768 tokens, 32/8 heads of 128, groups of 32: 1.22 GB in
+// 259 to 277 us, 4.4 to 4.7 TB/s, 0.67 to 0.72 of the measured copy rate.  The arithmetic
+// without the copies takes 241 to 246 us, the copies without the arithmetic 208
+// (an earlier form, of eight warps): issue bounds it.  37 sequences of 16384
+// tokens: 690 instructions a tile, 0.66 of the issue slots, 0.51 of the ALU pipe,
+// 0.55 of DRAM.  Of the arithmetic, K's way to an operand costs about 23 us, V's
+// 36, the scaling and transposition of P 10, the exponentials 5, the products
+// themselves next to nothing.  8 x 4096: 18.7 us; one sequence of 65536: 29 us, of
+// 777: 10.5 us, of which 3.5 pass before the first tile is read.
 // Included by tilemix_kv4.cu.
 #pragma once
 
@@ -55,7 +71,9 @@ constexpr int kAttnKeys = 32;  // keys of a tile
 template <int NB>
 constexpr int kAttnWarps = NB == 1 ? 12 : 8;
 constexpr int kAttnMaxCtas = 160;  // at least one per SM (148 on a B200)
-constexpr int kAttnMinTiles = 8;  // tiles a CTA takes at least, while there are any
+// Tiles a CTA takes at least, while there are any (16: one sequence of 777 11.7 us
+// for 10.5).
+constexpr int kAttnMinTiles = 8;
 
 template <int D, int GROUP, int NB>
 struct AttnTile {
@@ -411,28 +429,28 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         run = in_tiles - in_t;
         in_t = in_tiles;
       } else {
-      // a page outside the pool is reported, and page 0 read in its place
-      int lo = page_next, hi = page_next;
-      if (page_sh == 4) {
-        // two pages; the second sixteen may have no key to see: then the first again
-        run = 1;
-        if (key + 16 < in_keys) hi = __ldg(in_table + (key >> 4) + 1);
-      } else {
-        run = min((page_1 + 1 - (key & page_1)) / kAttnKeys, (in_keys - key + kAttnKeys - 1) / kAttnKeys);
-      }
-      if (static_cast<unsigned>(lo) >= static_cast<unsigned>(p.pool.num_pages) ||
-          static_cast<unsigned>(hi) >= static_cast<unsigned>(p.pool.num_pages)) {
-        atomicOr(&g_kv4_status, kStatusBadPages);
-        lo = hi = 0;
-      }
-      const size_t row_lo = ((static_cast<size_t>(lo) * p.pool.hk + in_kv) << page_sh) + (key & page_1);
-      const size_t row_hi = page_sh == 4 ? (static_cast<size_t>(hi) * p.pool.hk + in_kv) << 4 : row_lo + 16;
-      k_lo = p.pool.k_codes + row_lo * (D / 2) + lane * 16;
-      k_hi = p.pool.k_codes + row_hi * (D / 2) + lane * 16;
-      sc = sc_src + (sc_half ? row_hi : row_lo) * (2 * kNg);
-      in_t += run;
-      const int then = in_t * kAttnKeys;
-      if (then < in_keys) page_next = __ldg(in_table + (then >> page_sh));
+        // a page outside the pool is reported, and page 0 read in its place
+        int lo = page_next, hi = page_next;
+        if (page_sh == 4) {
+          // two pages; the second sixteen may have no key to see: then the first again
+          run = 1;
+          if (key + 16 < in_keys) hi = __ldg(in_table + (key >> 4) + 1);
+        } else {
+          run = min((page_1 + 1 - (key & page_1)) / kAttnKeys, (in_keys - key + kAttnKeys - 1) / kAttnKeys);
+        }
+        if (static_cast<unsigned>(lo) >= static_cast<unsigned>(p.pool.num_pages) ||
+            static_cast<unsigned>(hi) >= static_cast<unsigned>(p.pool.num_pages)) {
+          atomicOr(&g_kv4_status, kStatusBadPages);
+          lo = hi = 0;
+        }
+        const size_t row_lo = ((static_cast<size_t>(lo) * p.pool.hk + in_kv) << page_sh) + (key & page_1);
+        const size_t row_hi = page_sh == 4 ? (static_cast<size_t>(hi) * p.pool.hk + in_kv) << 4 : row_lo + 16;
+        k_lo = p.pool.k_codes + row_lo * (D / 2) + lane * 16;
+        k_hi = p.pool.k_codes + row_hi * (D / 2) + lane * 16;
+        sc = sc_src + (sc_half ? row_hi : row_lo) * (2 * kNg);
+        in_t += run;
+        const int then = in_t * kAttnKeys;
+        if (then < in_keys) page_next = __ldg(in_table + (then >> page_sh));
       }
     };
 

@@ -7,10 +7,12 @@
 // page and each slot is independent of all others and finds its sequence by
 // bisection, so long prompts spread over all threads whatever their number.
 //
-// The work is a few hundred kilobytes at most: latency bounds it, not bytes.
-// One launch does it all.  A cluster of CTAs shares the slots of large calls
-// (its barrier orders the stack's writes before its reads); the tables' pages
-// need no ordering against the slots, which compute their page from the stack.
+// The work is a few hundred kilobytes at most: latency bounds it, not bytes (256
+// sequences of one token 4.2 us, 125,000 slots of 64 prompts 7.2 us, their
+// rollback 10 us).  One launch does it all.  A cluster of sixteen CTAs shares the
+// slots of large calls (eight: 10.7 us; a cluster for 256 tokens: 4.6 us for 4.2);
+// its barrier orders the stack's writes before its reads, and the slots need none
+// against the tables, as they compute their page from the stack.
 // Included by tilemix_kv4.cu.
 #pragma once
 

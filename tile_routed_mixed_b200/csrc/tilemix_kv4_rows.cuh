@@ -15,14 +15,25 @@
 // 2^-12 moves no quotient across a half-integer and puts every tie exactly
 // on one, and the second rounding (to an integer, ties to even) gives
 // rne(x / s) as IEEE division would.
+//
+// Measured (B200): 32768 tokens of 8 heads of 128 in, 174 MB in 36 us; out
+// again 37 us; 12 ragged sequences of up to 16384 tokens of 4 heads out, 243 MB
+// in 49 us: 4.7 to 4.9 TB/s, 0.73 to 0.75 of the measured copy rate.  What bounds
+// them is instructions beside the bytes (0.77 to 0.85 of the issue slots when a
+// chunk found its token, head and place by itself: 48 and 45 us): so a thread
+// keeps one place of a row over its tokens, quotients outside +-7 and subnormal
+// scales have a path of their own, and a product of code and scale is one packed
+// multiplication in the type, rounded once.
 // Included by tilemix_kv4.cu.
 #pragma once
 
 namespace tilemix {
 
 constexpr int kRowThreads = 256;
-// Chunks from which a thread takes four (of fewer, one each spreads them over
-// more SMs): two full waves of one each.
+// Chunks from which a thread takes four tokens, loaded together: two full waves
+// of one each.  Above, one / four: 32768 tokens in 49 / 36 us, out 58 / 37, the
+// ragged batch out 78 / 49.  Below, one each spreads the rows over more SMs: 8
+// tokens in 1.3 / 1.8 us, one sequence of 1000 out 1.9 / 2.3.
 constexpr long long kRowsWide = 148LL * 2048 * 2;
 
 namespace kv4 {

@@ -16,11 +16,11 @@
 // on one, and the second rounding (to an integer, ties to even) gives
 // rne(x / s) as IEEE division would.
 //
-// Measured (B200): 32768 tokens of 8 heads of 128 in, 174 MB in 36 us; out
+// Measured (B200): 32768 tokens of 8 heads of 128 in, 172 MB in 36 us; out
 // again 37 us; 12 ragged sequences of up to 16384 tokens of 4 heads out, 243 MB
-// in 49 us: 4.7 to 4.9 TB/s, 0.73 to 0.75 of the measured copy rate.  What bounds
-// them is instructions beside the bytes (0.77 to 0.85 of the issue slots when a
-// chunk found its token, head and place by itself: 48 and 45 us): so a thread
+// in 49 us: 4.7 to 4.9 TB/s, 0.72 to 0.75 of the measured copy rate.  Issue bounds
+// them: 0.78 of the slots (ALU 0.67 in, 0.77 out), DRAM below a half.  Before (48
+// and 45 us) a chunk found its token, head and place by itself: so a thread
 // keeps one place of a row over its tokens, quotients outside +-7 and subnormal
 // scales have a path of their own, and a product of code and scale is one packed
 // multiplication in the type, rounded once.

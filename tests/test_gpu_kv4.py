@@ -665,3 +665,32 @@ def test_rows_of_one_page_in_many_sequences():
     pool.table[1, :2] = pool.table[0, :2]
     pool.table[2, :2] = pool.table[0, :2]
     _attend(pool, [1, 1, 2], 2)
+
+
+def test_plans_of_very_different_sizes_from_two_threads():
+    """What one call asks of the kernel does not depend on another's size."""
+    import threading
+    import tile_routed_mixed_b200 as tm
+    sizes = [1, tm.PAGE_PLAN_MAX_SEQS]
+    caches = [tm.TileMixKV4Cache(n, 16, 1, 64, n, 1) for n in sizes]
+    news = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in sizes]
+    outs = [c.new_plan(16) for c in caches]
+    failed = []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5000):
+                    caches[i].plan(news[i], out=outs[i])
+        except RuntimeError as e:
+            failed.append((sizes[i], e))
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    assert tm.tilemix_get_error() == 0

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tilemix.h"
 #include "tilemix_internal.h"
 #include "tilemix_kv4.h"
 #include "tilemix_mma.cuh"

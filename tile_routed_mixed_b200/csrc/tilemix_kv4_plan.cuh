@@ -247,8 +247,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PagePlanP
 
 int launch_page_plan(const PagePlanParams& p, cudaStream_t stream) {
   const int smem = 5 * static_cast<int>(sizeof(int)) * p.nseq;
-  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The limit belongs to the function, not to the call: every call sets the same
+  // one, so that a small call of another thread takes nothing from a large one.
+  cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       5 * static_cast<int>(sizeof(int)) * TILEMIX_PAGE_PLAN_MAX_SEQS);
   if (e != cudaSuccess) return static_cast<int>(e);
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr{};

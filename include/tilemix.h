@@ -644,8 +644,10 @@ int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
  *   O = softmax(scale * q . K^T) V over the values the codes stand for;
  *   scores, softmax and O's sums in fp32 (the codes are exact operands of the
  *   matrix products, q is used to at least 11 bits below its row's largest
- *   magnitude, each probability times its V scale is rounded once to 11 bits),
- *   O rounded once to the cache's type.
+ *   magnitude, each probability times its V scale is rounded once to 11 bits, or
+ *   to 2^-30 of the largest V scale met where that is coarser), O rounded once
+ *   to the cache's type.  A row that is not finite reaches the queries that
+ *   attend to it, and no others.
  * A query with no position to attend to gets O = 0 and an LSE of -infinity.  A
  * sequence with no queries reads nothing.  A table entry that names no page is
  * reported by tilemix_get_error() as INVALID_ARG; what its sequence gets is then

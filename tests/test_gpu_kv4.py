@@ -694,3 +694,28 @@ def test_plans_of_very_different_sizes_from_two_threads():
     torch.cuda.synchronize()
     assert not failed, failed
     assert tm.tilemix_get_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("d,group,rep", [(128, 32, 1), (128, 64, 2), (128, 128, 5), (64, 32, 5), (64, 64, 1)])
+@pytest.mark.parametrize("length", [3, 33, 60, 700])
+def test_attend_not_finite_rows_of_later_tokens(dtype, d, group, rep, length):
+    """A new token's row that is not finite reaches its own query and later ones,
+    not those in front of it."""
+    rng = np.random.default_rng(31)
+    new = 3
+    pool = kc.Pool(rng, [length], 2, d, group, 16, dtype)
+    for back, w, head, i in ((1, "v", 0, 0), (2, "v", 1, d // group - 1), (1, "k", 1, 0)):
+        pos = length - back
+        pool.scales[w][pool.table[0, pos // 16], head, pos % 16, i] = np.nan
+    q = kc.draw(rng, (new, 2 * rep, d), dtype)
+    o, lse = pool.cache().attend(kc.to_device(q, dtype), length, token_start=_i32([0, new]), max_new=new, lse=True)
+    o, lse = kc.to_numpy(o), kc.to_numpy(lse).T
+    k, v = pool.row("k", 0), pool.row("v", 0)
+    want, wlse, mag, reach = okv.attend(q, k, v, new)
+    assert np.array_equal(np.isnan(o), np.isnan(want))
+    assert np.array_equal(np.isnan(lse), np.isnan(wlse))
+    do, dl = kc.attend_bounds(want, wlse, mag, reach, dtype, np.nanmax(np.abs(v)) / 7, length)
+    seen, fin = ~np.isnan(want), ~np.isnan(wlse)
+    assert (np.abs(o - want)[seen] <= do[seen]).all()
+    assert (np.abs(lse - wlse)[fin] <= dl[fin]).all()

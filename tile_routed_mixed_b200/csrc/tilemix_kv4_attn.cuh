@@ -672,6 +672,57 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
                 for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = 0u;
               }
             }
+          // A NaN among V's scales of keys that only some columns see: the masked
+          // ones' zero probabilities would carry it on.  It goes to the outputs of
+          // the columns that do see its key, and out of the product.
+          bool odd_one = false;
+#pragma unroll
+          for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < (kNg + 1) / 2; ++i) {
+                const float2 f = kv4::unpack2<BF16>(vsc[mb][h][i]);
+                odd_one |= (isnan(f.x) || isnan(f.y)) && key0 + 16 * mb + 8 * h + key_g >= min_lim;
+              }
+          if (__any_sync(0xffffffffu, odd_one)) {
+#pragma unroll
+            for (int i = 0; i < kNg; ++i) {
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  bool hit = false;
+#pragma unroll
+                  for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                      const int key = key0 + 16 * mb + 8 * h + key_g;
+                      const float2 f = kv4::unpack2<BF16>(vsc[mb][h][i / 2]);
+                      hit |= isnan((i & 1) ? f.y : f.x) && key >= min_lim && key < lim[nb][j];
+                    }
+                  // the lanes that hold the same columns
+                  if (__ballot_sync(0xffffffffu, hit) & (0x11111111u << q4)) {
+#pragma unroll
+                    for (int t = i * kTg; t < (i + 1) * kTg; ++t)
+#pragma unroll
+                      for (int x = 0; x < 2; ++x)
+                        o[t][x][nb][j] = o[t][x][nb][2 + j] = __int_as_float(0x7fffffff);
+                  }
+                }
+            }
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                if (key0 + 16 * mb + 8 * h + key_g >= min_lim) {
+#pragma unroll
+                  for (int i = 0; i < (kNg + 1) / 2; ++i) {
+                    const float2 f = kv4::unpack2<BF16>(vsc[mb][h][i]);
+                    vsc[mb][h][i] &= (isnan(f.x) ? 0u : 0xffffu) | (isnan(f.y) ? 0u : 0xffff0000u);
+                  }
+                }
+          }
         }
 
         // running maximum, and the power of two of V's scales

@@ -49,10 +49,10 @@
 //
 // Measured (B200; from a graph of calls over three caches in turn): 64 ragged
 // sequences of up to 32768 tokens, 32/8 heads of 128, groups of 32: 1.22 GB in
-// 257 to 268 us, 4.6 to 4.7 TB/s, 0.70 to 0.72 of the measured copy rate (up to
-// 289 us as single calls after seconds of other work).  The
-// arithmetic without the copies takes 241 to 246 us, the copies without the
-// arithmetic 208 (an earlier form, of eight warps): issue bounds it.  37 sequences of 16384
+// 257 to 268 us, 4.5 to 4.7 TB/s, 0.70 to 0.72 of the measured copy rate (262 to
+// 289 us as single calls, in turn with a plain form).  The arithmetic without the
+// copies takes 241 to 246 us, the copies without the arithmetic 208 (an earlier
+// form, of eight warps): issue bounds it.  37 sequences of 16384
 // tokens: 690 instructions a tile, 0.66 of the issue slots, 0.51 of the ALU pipe,
 // 0.55 of DRAM.  Of the arithmetic, K's way to an operand costs about 23 us, V's
 // 36, the scaling and transposition of P 10, the exponentials 5, the products

@@ -1,0 +1,99 @@
+"""GPU parity of the 4-bit attention over the whole range of the cache's types:
+V scales, K scales and scores of every magnitude that append can write."""
+import numpy as np
+import pytest
+
+from oracle import kv4 as okv
+
+torch = pytest.importorskip("torch")
+from tests import kv4_cases as kc  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    import tile_routed_mixed_b200 as tm
+    assert tm.tilemix_get_error() == tm.OK
+
+
+def _fill(pool, which, scale_of):
+    """Rows of `which` with magnitudes scale_of(position) (an array per sequence)."""
+    rng = np.random.default_rng(97)
+    for s, n in enumerate(pool.lengths):
+        x = np.clip(rng.standard_normal((n, pool.hk, pool.d)), -3.9, 3.9)
+        x = okv.round_to(x * np.asarray(scale_of(np.arange(n), n), dtype=np.float64)[:, None, None], pool.dtype)
+        c, sc = okv.quantise(x, pool.group, pool.dtype)
+        pages, rows = pool.table[s, np.arange(n) // pool.page], np.arange(n) % pool.page
+        pool.codes[which][pages, :, rows] = c
+        pool.scales[which][pages, :, rows] = sc
+
+
+def _largest(pool, s, queries):
+    """The largest V scale that each query meets, [queries, 1, 1]."""
+    n = pool.lengths[s]
+    pages, rows = pool.table[s, np.arange(n) // pool.page], np.arange(n) % pool.page
+    top = pool.scales["v"][pages, :, rows].max(axis=(1, 2))
+    return np.array([top[:max(0, n - queries + i + 1)].max(initial=0.0) for i in range(queries)])[:, None, None]
+
+
+def _check(pool, queries, hq, q_scale=1.0, scale=0.0, seed=5):
+    """Attention of the last queries[s] tokens against the oracle, within the
+    bound of kv4_cases with each query's own largest V scale (and half a step of
+    a subnormal bf16 output)."""
+    rng = np.random.default_rng(seed)
+    start = np.concatenate([[0], np.cumsum(queries)])
+    q = kc.draw(rng, (int(start[-1]), hq, pool.d), pool.dtype, q_scale)
+    start_d = torch.tensor(start.tolist(), dtype=torch.int32, device="cuda")
+    o, lse = pool.cache().attend(kc.to_device(q, pool.dtype), max(pool.lengths), token_start=start_d,
+                                 max_new=max(queries), softmax_scale=scale, lse=True)
+    o, lse = kc.to_numpy(o), kc.to_numpy(lse).T
+    for s, n in enumerate(pool.lengths):
+        a, b = start[s], start[s + 1]
+        want, wlse, mag, reach = okv.attend(q[a:b], pool.row("k", s), pool.row("v", s), b - a, scale or None)
+        do, dl = kc.attend_bounds(want, wlse, mag, reach, pool.dtype, _largest(pool, s, b - a), n)
+        do = do + 2.0 ** -134
+        assert np.isfinite(o[a:b]).all() and np.isfinite(lse[a:b]).all(), s
+        assert (np.abs(o[a:b] - want) <= do).all(), (s, float((np.abs(o[a:b] - want) / do).max()))
+        assert (np.abs(lse[a:b] - wlse) <= dl).all(), s
+
+
+SHAPES = [(128, 32, 1, [1, 1]), (128, 128, 2, [3, 1]), (64, 32, 2, [7, 2]), (128, 64, 5, [5, 3])]
+
+
+@pytest.mark.parametrize("d,group,rep,queries", SHAPES)
+@pytest.mark.parametrize("power", [-126, -110, -95, -88, -70, -60, 60, 93, 97, 104, 115, 125])
+def test_values_of_one_magnitude(d, group, rep, queries, power):
+    """All of V near one power of two, from the smallest normal bf16 to the largest."""
+    rng = np.random.default_rng(1)
+    pool = kc.Pool(rng, [40, 1500], 2, d, group, 32, "bf16")
+    _fill(pool, "v", lambda at, n: np.full(n, 2.0 ** power))
+    _check(pool, queries, 2 * rep)
+
+
+@pytest.mark.parametrize("d,group,rep,queries", SHAPES)
+@pytest.mark.parametrize("turn", ["grow", "fall", "zeros_first", "zeros_last"])
+def test_values_of_all_magnitudes(d, group, rep, queries, turn):
+    """V from 2^-120 to 2^120 along a sequence, either way, and rows of zeros
+    before or behind tiny and huge ones: partial results of very different units
+    are joined."""
+    rng = np.random.default_rng(2)
+    pool = kc.Pool(rng, [200, 2500], 2, d, group, 16, "bf16")
+
+    def scale_of(at, n):
+        if turn == "grow":
+            return 2.0 ** (at * 240 // n - 120.0)
+        if turn == "fall":
+            return 2.0 ** (120.0 - at * 240 // n)
+        half = (at < n // 2) == (turn == "zeros_first")
+        return np.where(half, 0.0, 2.0 ** np.where(at % 2 == 0, 110.0, -110.0) if n > 1000 else 2.0 ** -115)
+
+    _fill(pool, "v", scale_of)
+    _check(pool, queries, 2 * rep)

@@ -38,7 +38,10 @@
 // probabilities are 2^(score - r) with r = the largest score + log2 of the largest V scale (its
 // power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
 // a score passes the old largest by 8 or a scale doubles: P s_v stays below
-// 2^14, and fp32 holds the sums.  r cancels between O and the sum.
+// 2^14, and fp32 holds the sums.  r cancels between O and the sum.  Where
+// bf16's largest V scale leaves 2^-90 .. 2^93, probabilities would leave fp32:
+// V's scales are then moved to the nearer end by a power of two, tile by tile in the branch
+// that moves r, and O back at the unit's end.
 //
 // Layouts.  With MMA fragments (rows g and g + 8, column pairs q4) a lane's
 // operands of K are D / 32 words of a key's row, 16 (or 8) bytes together in
@@ -147,6 +150,38 @@ __device__ __forceinline__ float sum_over_rows(float x) {
   x += __shfl_xor_sync(0xffffffffu, x, 4);
   x += __shfl_xor_sync(0xffffffffu, x, 8);
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Powers of two that the largest V scale takes part in a column's reference with;
+// beyond them (bf16 only) the scales are moved by v_shift.  2^95 times 2^8 times
+// the keys of a warp, and 2^-88 less 38 bits, are still fp32.
+constexpr int kVLow = -90, kVHigh = 93;
+constexpr int kVNone = -200;  // no V scale but zeros so far
+// fp16's scales have no small ones to tell from zeros: the least is taken as 2^-60.
+template <bool BF16>
+constexpr int kVStart = BF16 ? kVNone : -60;
+__device__ __forceinline__ int power_of(float x) {  // of x >= 0
+  return x > 0.f ? max(static_cast<int>(min(__float_as_uint(x) >> 23, 253u)), 1) - 127 : kVNone;
+}
+__device__ __forceinline__ float two_to(int e) {  // e in -126 .. 127
+  return __int_as_float((e + 127) << 23);
+}
+template <bool BF16>
+__device__ __forceinline__ int v_shift(int top) {
+  if (!BF16 || top == kVNone) return 0;
+  return top > kVHigh ? top - kVHigh : min(top - kVLow, 0);
+}
+// A largest V scale of 2^(top + 1) or more moves the reference; all do while
+// scales have to be moved.
+template <bool BF16>
+__device__ __forceinline__ float v_limit(int top) {
+  if (v_shift<BF16>(top) != 0) return -1.0f;
+  return top == kVNone ? 0x1p-133f : two_to(top + 1);
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t times2(uint32_t pair, float f) {
+  const float2 x = unpack2<BF16>(pair);
+  return pack2<BF16>(x.x * f, x.y * f);
 }
 
 // What the schedule needs to know about a sequence.
@@ -308,6 +343,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   __shared__ int holders[2][2];
   __shared__ int state_of[2 * kWarps];
   __shared__ int last_here[2];  // states to combine, if this CTA is the last to arrive
+  __shared__ int v_top[kWarps];  // power of two of the largest V scale of a warp's unit
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
@@ -563,9 +599,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // ---- its running state ----
       float o[kT][2][NB][4];
       // per column: the reference r of its probabilities 2^(score - r), the score
-      // that moves it, their sum; per unit: the power of two of V's scales
+      // that moves it, their sum; per unit: the V scale that moves it
       float r[NB][2], mv[NB][2], l[NB][2];
-      float sig = 0x1p-60f;
+      float v_lim = kv4::v_limit<BF16>(kv4::kVStart<BF16>);
+      __syncwarp();
+      if (lane == 0) v_top[warp] = kv4::kVStart<BF16>;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -743,12 +781,25 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           vm = kv4::max2<BF16>(vm, vsc[x & 1][(x >> 1) & 1][x >> 2]);
         const float2 vm2 = kv4::unpack2<BF16>(vm);  // (one scale per row: the upper half is zero)
         float vmax = fmaxf(vm2.x, vm2.y);
-        moved |= vmax >= 2.0f * sig;
+        moved |= !(vmax < v_lim);
         if (__any_sync(0xffffffffu, moved)) {
-          vmax = kv4::max_over_rows(vmax);
-          const uint32_t ve = min(__float_as_uint(vmax) >> 23, 220u);
-          sig = fmaxf(sig, __uint_as_float(ve << 23));
-          const float lg = static_cast<float>(static_cast<int>(__float_as_uint(sig) >> 23) - 127);
+          const int top0 = v_top[warp];
+          const int top = max(top0, kv4::power_of(kv4::max_over_rows(vmax)));
+          const int shift = kv4::v_shift<BF16>(top), shifted = kv4::v_shift<BF16>(top0) - shift;
+          const float lg = static_cast<float>(max(top - shift, kv4::kVLow));
+          v_lim = kv4::v_limit<BF16>(top);
+          __syncwarp();
+          if (lane == 0) v_top[warp] = top;
+          if (shift != 0) {
+            const float f = kv4::two_to(-shift);
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < (kNg + 1) / 2; ++i)
+                  vsc[mb][h][i] = kv4::times2<BF16>(vsc[mb][h][i], f);
+          }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -756,7 +807,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
               // largest score so far; -infinity while no key was seen
               const float top_s = fmaxf(mv[nb][j] - 8.0f, kv4::max_over_rows(mx[nb][j]));
               const float to = top_s == -INFINITY ? r[nb][j] : top_s + lg - 5.0f;
-              const float ao = mv[nb][j] == -INFINITY ? 1.0f : ptx::ex2(r[nb][j] - to);
+              const bool first = mv[nb][j] == -INFINITY;
+              const float by = r[nb][j] - to, ao = first ? 1.0f : ptx::ex2(by);
+              const float bo = BF16 && !first ? ptx::ex2(by + static_cast<float>(shifted)) : ao;
               r[nb][j] = to;
               mv[nb][j] = top_s + 8.0f;
               l[nb][j] *= ao;
@@ -764,8 +817,8 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
               for (int t = 0; t < kT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  o[t][i][nb][j] *= ao;
-                  o[t][i][nb][2 + j] *= ao;
+                  o[t][i][nb][j] *= bo;
+                  o[t][i][nb][2 + j] *= bo;
                 }
             }
         }
@@ -835,6 +888,31 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur, part};
       }
       __syncwarp();
+      // References of states that are joined lie within 2^120 of one another (as far
+      // as their scores do), and sums of V, not yet divided, within fp32: so a
+      // state's unit is the V scales' between 2^-45 and 2^65, else the nearer end.
+      if constexpr (BF16) {
+        const int top = v_top[warp];
+        if (top < -45 || top > 65) {
+          const int shift = kv4::v_shift<BF16>(top), lg = max(top - shift, kv4::kVLow);
+          const int unit = min(max(lg + shift, -45), 65);
+          const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              l[nb][j] *= to_l;
+              r[nb][j] += static_cast<float>(unit - lg);
+#pragma unroll
+              for (int t = 0; t < kT; ++t)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  o[t][i][nb][j] *= to_o;
+                  o[t][i][nb][2 + j] *= to_o;
+                }
+            }
+        }
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll

@@ -97,3 +97,14 @@ def test_values_of_all_magnitudes(d, group, rep, queries, turn):
 
     _fill(pool, "v", scale_of)
     _check(pool, queries, 2 * rep)
+
+
+@pytest.mark.parametrize("dtype,group,rep,new,low,high", [("bf16", 32, 1, 1, -53, 110), ("bf16", 64, 4, 3, 0, 122),
+                                                          ("fp16", 64, 4, 3, -9, 14)])
+def test_values_that_jump(dtype, group, rep, new, low, high):
+    """One huge row behind many small ones, where a warp has several tiles: what
+    it had before keeps its share of the sum."""
+    lengths = [4000, 3970, 4100, 3900, 4050]
+    pool = kc.Pool(np.random.default_rng(6), lengths, 8, 64, group, 64, dtype)
+    _fill(pool, "v", lambda at, n: np.where(at == n // 3, 2.0 ** high, 2.0 ** low))
+    _check(pool, [new] * 5, 8 * rep)

@@ -808,10 +808,13 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
               const float top_s = fmaxf(mv[nb][j] - 8.0f, kv4::max_over_rows(mx[nb][j]));
               const float to = top_s == -INFINITY ? r[nb][j] : top_s + lg - 5.0f;
               const bool first = mv[nb][j] == -INFINITY;
-              const float by = r[nb][j] - to, ao = first ? 1.0f : ptx::ex2(by);
+              // (the sum may need a factor below fp32's range: from 2^95 to 2^-88)
+              const float by = r[nb][j] - to, down = BF16 && by < -100.0f ? 64.0f : 0.f;
+              const float ao = first ? 1.0f : ptx::ex2(by + down);
               const float bo = BF16 && !first ? ptx::ex2(by + static_cast<float>(shifted)) : ao;
               r[nb][j] = to;
               mv[nb][j] = top_s + 8.0f;
+              if (BF16) l[nb][j] *= down > 0.f ? 0x1p-64f : 1.0f;
               l[nb][j] *= ao;
 #pragma unroll
               for (int t = 0; t < kT; ++t)
@@ -888,14 +891,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur, part};
       }
       __syncwarp();
-      // References of states that are joined lie within 2^120 of one another (as far
-      // as their scores do), and sums of V, not yet divided, within fp32: so a
-      // state's unit is the V scales' between 2^-45 and 2^65, else the nearer end.
+      // References of states that are joined lie within 2^70 of one another (as far
+      // as their scores do: a weight below 2^-126 is lost), and sums of V, not yet
+      // divided, within fp32: so a state's unit is the V scales' between 2^-30 and
+      // 2^40, else the nearer end.
       if constexpr (BF16) {
         const int top = v_top[warp];
-        if (top < -45 || top > 65) {
+        if (top < -30 || top > 40) {
           const int shift = kv4::v_shift<BF16>(top), lg = max(top - shift, kv4::kVLow);
-          const int unit = min(max(lg + shift, -45), 65);
+          const int unit = min(max(lg + shift, -30), 40);
           const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)

@@ -108,3 +108,28 @@ def test_values_that_jump(dtype, group, rep, new, low, high):
     pool = kc.Pool(np.random.default_rng(6), lengths, 8, 64, group, 64, dtype)
     _fill(pool, "v", lambda at, n: np.where(at == n // 3, 2.0 ** high, 2.0 ** low))
     _check(pool, [new] * 5, 8 * rep)
+
+
+@pytest.mark.parametrize("dtype,own,later", [("bf16", 0, 40), ("bf16", 0, 62), ("bf16", 0, 98), ("bf16", 0, 125),
+                                             ("bf16", -50, 124), ("bf16", -100, 0), ("bf16", 100, 125),
+                                             ("fp16", -9, 13), ("fp16", -14, 0)])
+@pytest.mark.parametrize("d,group,rep,queries", [(128, 32, 1, 3), (128, 64, 4, 5), (64, 64, 2, 21), (64, 32, 1, 40)])
+@pytest.mark.parametrize("length", [45, 1300])
+def test_a_later_tokens_values_cost_earlier_queries_nothing(dtype, own, later, d, group, rep, queries, length):
+    """V rows that only the last queries see, far larger than the others: the
+    queries in front of them are as exact as without."""
+    rng = np.random.default_rng(3)
+    pool = kc.Pool(rng, [length], 2, d, group, 16, dtype)
+    _fill(pool, "v", lambda at, n: np.where(at < n - (queries + 1) // 2, 2.0 ** own, 2.0 ** later))
+    _check(pool, [queries], 2 * rep)
+
+
+def test_zeros_before_a_later_tokens_values():
+    """Queries that see rows of zeros only, and one that sees a huge row: as
+    outputs, and as partial results of several CTAs."""
+    for length in (50, 4000):
+        pool = kc.Pool(np.random.default_rng(4), [length], 1, 128, 32, 16, "bf16")
+        _fill(pool, "v", lambda at, n: np.where((at < n - 1) & (at > 40), 0.0, 2.0 ** 120))
+        _check(pool, [3], 2)
+        _fill(pool, "v", lambda at, n: np.where(at < n - 1, 0.0, 1.0))
+        _check(pool, [3], 2)

@@ -38,10 +38,12 @@
 // probabilities are 2^(score - r) with r = the largest score + log2 of the largest V scale (its
 // power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
 // a score passes the old largest by 8 or a scale doubles: P s_v stays below
-// 2^14, and fp32 holds the sums.  r cancels between O and the sum.  Where
-// bf16's largest V scale leaves 2^-90 .. 2^93, probabilities would leave fp32:
-// V's scales are then moved to the nearer end by a power of two, tile by tile in the branch
-// that moves r, and O back at the unit's end.
+// 2^14, and fp32 holds the sums.  r cancels between O and the sum.  In the
+// branch that moves r, apart from what most tiles need: where a unit's columns see
+// different keys, each column goes by the V scales that it sees; and where bf16's
+// largest V scale leaves 2^-90 .. 2^93, probabilities would leave fp32, so V's scales
+// are moved to the nearer end by a power of two, tile by tile, and O back at the
+// unit's end.  (The same per column in line: a step 51.5 us for 49.5.)
 //
 // Layouts.  With MMA fragments (rows g and g + 8, column pairs q4) a lane's
 // operands of K are D / 32 words of a key's row, 16 (or 8) bytes together in
@@ -155,33 +157,29 @@ __device__ __forceinline__ float sum_over_rows(float x) {
 // Powers of two that the largest V scale takes part in a column's reference with;
 // beyond them (bf16 only) the scales are moved by v_shift.  2^95 times 2^8 times
 // the keys of a warp, and 2^-88 less 38 bits, are still fp32.
-constexpr int kVLow = -90, kVHigh = 93;
-constexpr int kVNone = -200;  // no V scale but zeros so far
-// fp16's scales have no small ones to tell from zeros: the least is taken as 2^-60.
 template <bool BF16>
-constexpr int kVStart = BF16 ? kVNone : -60;
-__device__ __forceinline__ int power_of(float x) {  // of x >= 0
-  return x > 0.f ? max(static_cast<int>(min(__float_as_uint(x) >> 23, 253u)), 1) - 127 : kVNone;
+constexpr int kVLow = BF16 ? -90 : -60;  // (fp16's smallest is 2^-24: for zeros)
+constexpr int kVHigh = 93;
+constexpr int kVNone = -200;  // no V scale but zeros so far
+// A V scale from v_lim = 2^(the power of the largest so far + 1) on moves the
+// reference.  Marks: nothing seen yet; zeros seen; negative, see v_power.
+constexpr float kVStart = 0x1.8p-59f, kVZeros = 0x1p-133f;
+__device__ __forceinline__ int exponent(float x) {  // -127 for zeros and subnormals
+  return static_cast<int>(min(__float_as_uint(x) >> 23, 253u)) - 127;
 }
 __device__ __forceinline__ float two_to(int e) {  // e in -126 .. 127
   return __int_as_float((e + 127) << 23);
 }
-template <bool BF16>
 __device__ __forceinline__ int v_shift(int top) {
-  if (!BF16 || top == kVNone) return 0;
-  return top > kVHigh ? top - kVHigh : min(top - kVLow, 0);
+  if (top == kVNone) return 0;
+  return top > kVHigh ? top - kVHigh : min(top - kVLow<true>, 0);
 }
-// A largest V scale of 2^(top + 1) or more moves the reference; all do while
-// scales have to be moved.
-template <bool BF16>
-__device__ __forceinline__ float v_limit(int top) {
-  if (v_shift<BF16>(top) != 0) return -1.0f;
-  return top == kVNone ? 0x1p-133f : two_to(top + 1);
-}
-template <bool BF16>
-__device__ __forceinline__ uint32_t times2(uint32_t pair, float f) {
-  const float2 x = unpack2<BF16>(pair);
-  return pack2<BF16>(x.x * f, x.y * f);
+// A pair of scales times 2^e (e in -120 .. 126).
+__device__ __forceinline__ uint32_t move2(uint32_t pair, int e) {
+  const uint32_t f = static_cast<uint32_t>(e + 127) << 7;
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
+  return y;
 }
 
 // What the schedule needs to know about a sequence.
@@ -343,7 +341,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   __shared__ int holders[2][2];
   __shared__ int state_of[2 * kWarps];
   __shared__ int last_here[2];  // states to combine, if this CTA is the last to arrive
-  __shared__ int v_top[kWarps];  // power of two of the largest V scale of a warp's unit
+  // Of a warp's unit while v_lim is negative: the power of two of its largest V
+  // scale, and what the scales are moved by.
+  __shared__ int v_power[kWarps], v_moved[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
@@ -601,9 +601,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // per column: the reference r of its probabilities 2^(score - r), the score
       // that moves it, their sum; per unit: the V scale that moves it
       float r[NB][2], mv[NB][2], l[NB][2];
-      float v_lim = kv4::v_limit<BF16>(kv4::kVStart<BF16>);
-      __syncwarp();
-      if (lane == 0) v_top[warp] = kv4::kVStart<BF16>;
+      float v_lim = kv4::kVStart;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -783,22 +781,96 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         float vmax = fmaxf(vm2.x, vm2.y);
         moved |= !(vmax < v_lim);
         if (__any_sync(0xffffffffu, moved)) {
-          const int top0 = v_top[warp];
-          const int top = max(top0, kv4::power_of(kv4::max_over_rows(vmax)));
-          const int shift = kv4::v_shift<BF16>(top), shifted = kv4::v_shift<BF16>(top0) - shift;
-          const float lg = static_cast<float>(max(top - shift, kv4::kVLow));
-          v_lim = kv4::v_limit<BF16>(top);
-          __syncwarp();
-          if (lane == 0) v_top[warp] = top;
-          if (shift != 0) {
-            const float f = kv4::two_to(-shift);
+          vmax = kv4::max_over_rows(vmax);
+          const int power = max(kv4::exponent(v_lim) - 1, kv4::exponent(vmax));
+          const bool parted = key0 + kAttnKeys > min_lim && min_lim < keys;
+          float lg[NB][2];
 #pragma unroll
-            for (int mb = 0; mb < 2; ++mb)
+          for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(power);
+          if (v_lim < 0.f || (parted && (key0 >= min_lim || vmax >= v_lim)) ||
+              (BF16 && (power < kv4::kVLow<true> || power > kv4::kVHigh || vmax >= 0x1p70f * v_lim ||
+                        (v_lim == kv4::kVStart && vmax < v_lim)))) {
+            // ---- what hardly a tile needs ----
+            const bool marked = v_lim < 0.f, none = v_lim == kv4::kVStart || v_lim == kv4::kVZeros;
+            const int top0 = marked ? v_power[warp] : none ? kv4::kVNone : kv4::exponent(v_lim) - 1;
+            const int shift0 = marked ? v_moved[warp] : 0;
+            const int top = max(top0, vmax > 0.f ? max(kv4::exponent(vmax), -126) : kv4::kVNone);
+            const int shift = BF16 ? kv4::v_shift(top) : 0;
+            constexpr int kLow = kv4::kVLow<BF16>;
+            const int all0 = max(top0 - shift0, kLow), all = max(top - shift, kLow);
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+            for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(all);
+            if (parted) {
+              // Not all columns see all of the tile's keys: each goes by the scales that
+              // it does see, so that a later token's cost an earlier query no bits, and
+              // keeps its reference once its keys have ended.
+              uint32_t seen[NB];  // largest of a column pair
 #pragma unroll
-                for (int i = 0; i < (kNg + 1) / 2; ++i)
-                  vsc[mb][h][i] = kv4::times2<BF16>(vsc[mb][h][i], f);
+              for (int nb = 0; nb < NB; ++nb) seen[nb] = 0u;
+#pragma unroll
+              for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int key = key0 + 16 * mb + 8 * h + key_g;
+                  uint32_t x = vsc[mb][h][0];
+                  if constexpr (kNg == 4) x = kv4::max2<BF16>(x, vsc[mb][h][1]);
+                  x = kv4::max2<BF16>(x, __byte_perm(x, 0u, 0x1032));
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+                    seen[nb] = kv4::max2<BF16>(seen[nb], x & ((key < lim[nb][0] ? 0xffffu : 0u) |
+                                                              (key < lim[nb][1] ? 0xffff0000u : 0u)));
+                }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int by = 4; by < 32; by <<= 1)
+                  seen[nb] = kv4::max2<BF16>(seen[nb], __shfl_xor_sync(0xffffffffu, seen[nb], by));
+                const float2 f = kv4::unpack2<BF16>(seen[nb]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const float x = j ? f.y : f.x;
+                  if (lim[nb][j] <= key0)
+                    lg[nb][j] = r[nb][j] - (mv[nb][j] - 8.0f) + 5.0f;
+                  else if (lim[nb][j] < key0 + kAttnKeys)
+                    lg[nb][j] = static_cast<float>(
+                        max(max(top0, x > 0.f ? max(kv4::exponent(x), -126) : kv4::kVNone) - shift, kLow));
+                }
+              }
+            }
+            // the state in units of the new shift, and, where references jump, 2^64 lower
+            // (one factor could lie below fp32's range)
+            const int jump = all - all0 > 70 ? 64 : 0;
+            if (BF16 && (shift != shift0 || jump != 0)) {
+              const float fo = kv4::two_to(max(shift0 - shift - jump, -126)), fl = kv4::two_to(-jump);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  l[nb][j] *= fl;
+                  r[nb][j] += static_cast<float>(jump);
+#pragma unroll
+                  for (int t = 0; t < kT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                      o[t][i][nb][j] *= fo;
+                      o[t][i][nb][2 + j] *= fo;
+                    }
+                }
+            }
+            if (BF16 && shift != 0) {
+#pragma unroll
+              for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                  for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = kv4::move2(vsc[mb][h][i], -shift);
+            }
+            __syncwarp();
+            if (lane == 0) v_power[warp] = top, v_moved[warp] = shift;
+            // (negative: every tile from here to the unit's end)
+            v_lim = parted || shift != 0 ? -1.0f : top == kv4::kVNone ? kv4::kVZeros : kv4::two_to(top + 1);
+          } else {
+            v_lim = kv4::two_to(power + 1);
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -806,22 +878,17 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
             for (int j = 0; j < 2; ++j) {
               // largest score so far; -infinity while no key was seen
               const float top_s = fmaxf(mv[nb][j] - 8.0f, kv4::max_over_rows(mx[nb][j]));
-              const float to = top_s == -INFINITY ? r[nb][j] : top_s + lg - 5.0f;
-              const bool first = mv[nb][j] == -INFINITY;
-              // (the sum may need a factor below fp32's range: from 2^95 to 2^-88)
-              const float by = r[nb][j] - to, down = BF16 && by < -100.0f ? 64.0f : 0.f;
-              const float ao = first ? 1.0f : ptx::ex2(by + down);
-              const float bo = BF16 && !first ? ptx::ex2(by + static_cast<float>(shifted)) : ao;
+              const float to = top_s == -INFINITY ? r[nb][j] : top_s + lg[nb][j] - 5.0f;
+              const float ao = mv[nb][j] == -INFINITY ? 1.0f : ptx::ex2(r[nb][j] - to);
               r[nb][j] = to;
               mv[nb][j] = top_s + 8.0f;
-              if (BF16) l[nb][j] *= down > 0.f ? 0x1p-64f : 1.0f;
               l[nb][j] *= ao;
 #pragma unroll
               for (int t = 0; t < kT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  o[t][i][nb][j] *= bo;
-                  o[t][i][nb][2 + j] *= bo;
+                  o[t][i][nb][j] *= ao;
+                  o[t][i][nb][2 + j] *= ao;
                 }
             }
         }
@@ -895,27 +962,26 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // as their scores do: a weight below 2^-126 is lost), and sums of V, not yet
       // divided, within fp32: so a state's unit is the V scales' between 2^-30 and
       // 2^40, else the nearer end.
-      if constexpr (BF16) {
-        const int top = v_top[warp];
-        if (top < -30 || top > 40) {
-          const int shift = kv4::v_shift<BF16>(top), lg = max(top - shift, kv4::kVLow);
-          const int unit = min(max(lg + shift, -30), 40);
-          const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
+      if (BF16 && (v_lim < 0x1p-29f || v_lim > 0x1p41f)) {
+        const int shift = v_lim < 0.f ? v_moved[warp] : 0;
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              l[nb][j] *= to_l;
-              r[nb][j] += static_cast<float>(unit - lg);
+          for (int j = 0; j < 2; ++j) {
+            // the power in the column's reference
+            const int lg = mv[nb][j] == -INFINITY ? 0 : __float2int_rn(r[nb][j] - mv[nb][j] + 13.0f);
+            const int unit = min(max(lg + shift, -30), 40);
+            const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
+            l[nb][j] *= to_l;
+            r[nb][j] += static_cast<float>(unit - lg);
 #pragma unroll
-              for (int t = 0; t < kT; ++t)
+            for (int t = 0; t < kT; ++t)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  o[t][i][nb][j] *= to_o;
-                  o[t][i][nb][2 + j] *= to_o;
-                }
-            }
-        }
+              for (int i = 0; i < 2; ++i) {
+                o[t][i][nb][j] *= to_o;
+                o[t][i][nb][2 + j] *= to_o;
+              }
+          }
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)

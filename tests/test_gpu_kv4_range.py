@@ -133,3 +133,77 @@ def test_zeros_before_a_later_tokens_values():
         _check(pool, [3], 2)
         _fill(pool, "v", lambda at, n: np.where(at < n - 1, 0.0, 1.0))
         _check(pool, [3], 2)
+
+
+def _put(pool, which, s, x):
+    """Rows x [n, hk, d] as sequence s's K or V."""
+    n = pool.lengths[s]
+    c, sc = okv.quantise(okv.round_to(x, pool.dtype), pool.group, pool.dtype)
+    pages, rows = pool.table[s, np.arange(n) // pool.page], np.arange(n) % pool.page
+    pool.codes[which][pages, :, rows] = c
+    pool.scales[which][pages, :, rows] = sc
+
+
+SCORES = [("fp16", p) for p in (18, 22, 25, 26, 27, 28, 29, 31, 34)] + \
+         [("bf16", p) for p in (22, 26, 28, 30, 40, 70, 110)]
+
+
+@pytest.mark.parametrize("dtype,power", SCORES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("value", [2.0 ** -13, 1.0, 2.0 ** 12])
+def test_equal_scores_of_any_size(dtype, power, sign, value):
+    """Keys that are all the same, with scores (in powers of two) up to 2^power:
+    O is the mean of V, whatever the size of the scores (their rounding is the
+    same for all keys), the LSE the score itself to a rounding or two."""
+    d, rep, queries = 128, 2, [2, 1]
+    pool = kc.Pool(np.random.default_rng(7), [700, 33], 2, d, 32, 16, dtype)
+    _fill(pool, "v", lambda at, n: np.full(n, value))
+    size = 2.0 ** ((power - 4) / 2)            # d size^2 / sqrt(d) * log2(e) = 2^(4.03 + 2 log2(size))
+    for s, n in enumerate(pool.lengths):
+        _put(pool, "k", s, np.full((n, 2, d), size))
+    q = okv.round_to(np.full((3, 2 * rep, d), sign * size), dtype)
+    start = [0, 2, 3]
+    o, lse = pool.cache().attend(kc.to_device(q, dtype), 700, max_new=2, lse=True,
+                                 token_start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+    o, lse = kc.to_numpy(o), kc.to_numpy(lse).T
+    for s, n in enumerate(pool.lengths):
+        a, b = start[s], start[s + 1]
+        want, wlse, mag, _ = okv.attend(q[a:b], pool.row("k", s), pool.row("v", s), b - a)
+        do, _ = kc.attend_bounds(want, wlse, mag, np.zeros(wlse.shape), dtype, _largest(pool, s, b - a), n)
+        assert np.isfinite(o[a:b]).all()
+        assert (np.abs(o[a:b] - want) <= do).all(), float((np.abs(o[a:b] - want) / do).max())
+        assert (np.abs(lse[a:b] - wlse) <= 2.0 ** -18 + 2.0 ** -20 * np.abs(wlse)).all()
+
+
+# (channel 0 alone makes the score here: fp16 ends at 65504^2 / sqrt(128) * log2(e), 2^29)
+@pytest.mark.parametrize("dtype,power", [x for x in SCORES if x[0] == "bf16" or x[1] < 29])
+@pytest.mark.parametrize("rising", [False, True])
+def test_scores_that_differ_by_their_last_bits(dtype, power, rising):
+    """A large common score and small differences, at random or rising along the
+    sequence.  Rounded to fp32 many differences are gone, so all that can be asked
+    is a finite mean of V's rows with weights between zero and one, whose sum is one."""
+    d = 128
+    rng = np.random.default_rng(8)
+    pool = kc.Pool(rng, [1500, 64], 1, d, 32, 32, dtype)
+    size = 2.0 ** ((power + 3) / 2)
+    q = np.zeros((3, 2, d))
+    q[..., 0], q[..., 40] = size, 1.0
+    q = okv.round_to(q, dtype)
+    for s, n in enumerate(pool.lengths):
+        x = np.zeros((n, 1, d))
+        x[..., 0] = size
+        x[:, 0, 40] = np.linspace(-2000, 2000, n) if rising else rng.uniform(-2000, 2000, n)
+        _put(pool, "k", s, x)
+        v = np.clip(rng.standard_normal((n, 1, d)), -3, 3) * 2.0 ** -13
+        v[..., 100:] = 2.0 ** -13              # the same in all rows: the sum of the weights
+        _put(pool, "v", s, v)
+    start = [0, 2, 3]
+    o = pool.cache().attend(kc.to_device(q, dtype), 1500, max_new=2,
+                            token_start=torch.tensor(start, dtype=torch.int32, device="cuda"))
+    o = kc.to_numpy(o)
+    assert np.isfinite(o).all()
+    for s, n in enumerate(pool.lengths):
+        for i in range(start[s], start[s + 1]):
+            v = pool.row("v", s)[:n - (start[s + 1] - i) + 1, 0]
+            slack = 2.0 ** -6 * np.abs(v).max()    # bf16's rounding, P s_v's and the sums'
+            assert (o[i] >= v.min(axis=0) - slack).all() and (o[i] <= v.max(axis=0) + slack).all()

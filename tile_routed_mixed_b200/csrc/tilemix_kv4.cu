@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "tilemix.h"
 #include "tilemix_internal.h"
 #include "tilemix_kv4.h"

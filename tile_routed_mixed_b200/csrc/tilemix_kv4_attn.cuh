@@ -38,12 +38,14 @@
 // probabilities are 2^(score - r) with r = the largest score + log2 of the largest V scale (its
 // power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
 // a score passes the old largest by 8 or a scale doubles: P s_v stays below
-// 2^14, and fp32 holds the sums.  r cancels between O and the sum.  In the
-// branch that moves r, apart from what most tiles need: where a unit's columns see
-// different keys, each column goes by the V scales that it sees; and where bf16's
-// largest V scale leaves 2^-90 .. 2^93, probabilities would leave fp32, so V's scales
-// are moved to the nearer end by a power of two, tile by tile, and O back at the
-// unit's end.  (The same per column in line: a step 51.5 us for 49.5.)
+// 2^14, and fp32 holds the sums.  r cancels between O and the sum.  That serves
+// scores below 2^22 and V scales within 2^-30 .. 2^40 that do not grow fourfold
+// in keys that only some columns of a unit see.  A warp that meets anything else
+// takes the unit's remaining tiles in a second, wide form of the tile: there each
+// column goes by the V scales that it sees, bf16's largest and smallest are moved
+// by a power of two, and large scores are taken against the largest before their
+// rounding can matter.  (It costs plain calls what more code costs: 8 x 4096 19.0
+// us for 18.6, a step 49.5 for 48.1; in one form, behind branches, 18.9 and 50.6.)
 //
 // Layouts.  With MMA fragments (rows g and g + 8, column pairs q4) a lane's
 // operands of K are D / 32 words of a key's row, 16 (or 8) bytes together in
@@ -154,18 +156,24 @@ __device__ __forceinline__ float sum_over_rows(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Powers of two that the largest V scale takes part in a column's reference with;
-// beyond them (bf16 only) the scales are moved by v_shift.  2^95 times 2^8 times
-// the keys of a warp, and 2^-88 less 38 bits, are still fp32.
+// Powers of two that the largest V scale takes part in a column's reference with.
+// Within kVPlain, references of any two partial states lie so near that no weight
+// is lost, and sums of V within fp32.  Beyond (bf16 only) scales are moved by
+// v_shift to where 2^95 times 2^8 times the keys of a warp, and 2^-88 less 38 bits,
+// are still fp32.
+constexpr int kVPlainLow = -30, kVPlainHigh = 40;
 template <bool BF16>
 constexpr int kVLow = BF16 ? -90 : -60;  // (fp16's smallest is 2^-24: for zeros)
 constexpr int kVHigh = 93;
 constexpr int kVNone = -200;  // no V scale but zeros so far
 // A V scale from v_lim = 2^(the power of the largest so far + 1) on moves the
-// reference.  Marks: nothing seen yet; zeros seen; negative, see v_power.
-constexpr float kVStart = 0x1.8p-59f, kVZeros = 0x1p-133f;
+// reference; this before the first.
+constexpr float kVStart = 0x1.8p-59f;
 __device__ __forceinline__ int exponent(float x) {  // -127 for zeros and subnormals
   return static_cast<int>(min(__float_as_uint(x) >> 23, 253u)) - 127;
+}
+__device__ __forceinline__ int power_of(float x) {  // of a largest scale
+  return x > 0.f ? max(exponent(x), -126) : kVNone;
 }
 __device__ __forceinline__ float two_to(int e) {  // e in -126 .. 127
   return __int_as_float((e + 127) << 23);
@@ -174,11 +182,15 @@ __device__ __forceinline__ int v_shift(int top) {
   if (top == kVNone) return 0;
   return top > kVHigh ? top - kVHigh : min(top - kVLow<true>, 0);
 }
-// A pair of scales times 2^e (e in -120 .. 126).
+// A pair of scales times 2^e (e in -121 .. 126; fp16: -11 .. 15).
+template <bool BF16>
 __device__ __forceinline__ uint32_t move2(uint32_t pair, int e) {
-  const uint32_t f = static_cast<uint32_t>(e + 127) << 7;
+  const uint32_t f = BF16 ? static_cast<uint32_t>(e + 127) << 7 : static_cast<uint32_t>(e + 15) << 10;
   uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
+  if constexpr (BF16)
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
+  else
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
   return y;
 }
 
@@ -322,6 +334,14 @@ __device__ __forceinline__ void store_column(const Kv4AttnParams& p, const Unit&
 
 }  // namespace kv4
 
+// What a warp keeps of a unit beside its state once it is in the wide form.
+template <int NB>
+struct Beyond {
+  int top, shift;     // power of two of the largest V scale; what V's scales are moved by
+  bool against;       // scores are taken against raw
+  float raw[NB][2];   // the largest score of each column, before cs
+};
+
 template <int D, int GROUP, int NB, bool BF16>
 __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
     kv4_attn_kernel(const __grid_constant__ Kv4AttnParams p) {
@@ -341,9 +361,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   __shared__ int holders[2][2];
   __shared__ int state_of[2 * kWarps];
   __shared__ int last_here[2];  // states to combine, if this CTA is the last to arrive
-  // Of a warp's unit while v_lim is negative: the power of two of its largest V
-  // scale, and what the scales are moved by.
-  __shared__ int v_power[kWarps], v_moved[kWarps];
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;
@@ -602,6 +619,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // that moves it, their sum; per unit: the V scale that moves it
       float r[NB][2], mv[NB][2], l[NB][2];
       float v_lim = kv4::kVStart;
+      Beyond<NB> far;
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -615,16 +633,25 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         l[nb][0] = l[nb][1] = 0.f;
       }
 
-#pragma unroll 1
-      for (int it = 0; it < n; ++it) {
+      const uint8_t* st = nullptr;
+      const auto next_tile = [&]() {
         kv4::cp_wait<kStages - 2>();
         __syncwarp();  // this tile is here for all lanes, and the last one is read
         issue(stage == 0 ? kStages - 1 : stage - 1);
-        const uint8_t* st = ring + stage * Tile::kBytes;
+        st = ring + stage * Tile::kBytes;
         stage = stage == kStages - 1 ? 0 : stage + 1;
-        const int key0 = (t0 + it) * kAttnKeys;
-        if (key0 >= keys) continue;  // nothing of this tile was fetched
+      };
 
+      const auto row_scale = [](const uint32_t (&x)[(kNg + 1) / 2]) {  // the largest of a row
+        const float2 f = kv4::unpack2<BF16>(kNg == 4 ? kv4::max2<BF16>(x[0], x[(kNg - 1) / 2]) : x[0]);
+        return fmaxf(f.x, f.y);
+      };
+
+      // A tile's keys into the state.  Plain, it stops (false, the state as it was)
+      // where that would lose bits; `wide` is the form for all that hardly a tile
+      // needs, which runs from there to the unit's end.
+      const auto tile = [&](auto wide, int key0) -> bool {
+        constexpr bool kWide = decltype(wide)::value;
         // scores, to be scaled by cs
         float s[2][NB][4];
         uint32_t vsc[2][2][(kNg + 1) / 2];  // V's scales of rows g and g + 8
@@ -779,98 +806,127 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           vm = kv4::max2<BF16>(vm, vsc[x & 1][(x >> 1) & 1][x >> 2]);
         const float2 vm2 = kv4::unpack2<BF16>(vm);  // (one scale per row: the upper half is zero)
         float vmax = fmaxf(vm2.x, vm2.y);
-        moved |= !(vmax < v_lim);
+        moved |= kWide || !(vmax < v_lim);
         if (__any_sync(0xffffffffu, moved)) {
           vmax = kv4::max_over_rows(vmax);
-          const int power = max(kv4::exponent(v_lim) - 1, kv4::exponent(vmax));
           const bool parted = key0 + kAttnKeys > min_lim && min_lim < keys;
           float lg[NB][2];
+          if constexpr (!kWide) {
+            const int power = max(kv4::exponent(v_lim) - 1, kv4::exponent(vmax));
+            bool stop = BF16 && (power < kv4::kVPlainLow || power > kv4::kVPlainHigh);
+            // (scores from 2^22 on: no room for r's offset in their last bits, and a
+            // fused score - r keeps bits that the maximum has lost)
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(power);
-          if (v_lim < 0.f || (parted && (key0 >= min_lim || vmax >= v_lim)) ||
-              (BF16 && (power < kv4::kVLow<true> || power > kv4::kVHigh || vmax >= 0x1p70f * v_lim ||
-                        (v_lim == kv4::kVStart && vmax < v_lim)))) {
-            // ---- what hardly a tile needs ----
-            const bool marked = v_lim < 0.f, none = v_lim == kv4::kVStart || v_lim == kv4::kVZeros;
-            const int top0 = marked ? v_power[warp] : none ? kv4::kVNone : kv4::exponent(v_lim) - 1;
-            const int shift0 = marked ? v_moved[warp] : 0;
-            const int top = max(top0, vmax > 0.f ? max(kv4::exponent(vmax), -126) : kv4::kVNone);
-            const int shift = BF16 ? kv4::v_shift(top) : 0;
-            constexpr int kLow = kv4::kVLow<BF16>;
-            const int all0 = max(top0 - shift0, kLow), all = max(top - shift, kLow);
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(all);
-            if (parted) {
-              // Not all columns see all of the tile's keys: each goes by the scales that
-              // it does see, so that a later token's cost an earlier query no bits, and
-              // keeps its reference once its keys have ended.
-              uint32_t seen[NB];  // largest of a column pair
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) seen[nb] = 0u;
-#pragma unroll
-              for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int key = key0 + 16 * mb + 8 * h + key_g;
-                  uint32_t x = vsc[mb][h][0];
-                  if constexpr (kNg == 4) x = kv4::max2<BF16>(x, vsc[mb][h][1]);
-                  x = kv4::max2<BF16>(x, __byte_perm(x, 0u, 0x1032));
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb)
-                    seen[nb] = kv4::max2<BF16>(seen[nb], x & ((key < lim[nb][0] ? 0xffffu : 0u) |
-                                                              (key < lim[nb][1] ? 0xffff0000u : 0u)));
-                }
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-                for (int by = 4; by < 32; by <<= 1)
-                  seen[nb] = kv4::max2<BF16>(seen[nb], __shfl_xor_sync(0xffffffffu, seen[nb], by));
-                const float2 f = kv4::unpack2<BF16>(seen[nb]);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const float x = j ? f.y : f.x;
-                  if (lim[nb][j] <= key0)
-                    lg[nb][j] = r[nb][j] - (mv[nb][j] - 8.0f) + 5.0f;
-                  else if (lim[nb][j] < key0 + kAttnKeys)
-                    lg[nb][j] = static_cast<float>(
-                        max(max(top0, x > 0.f ? max(kv4::exponent(x), -126) : kv4::kVNone) - shift, kLow));
-                }
-              }
-            }
-            // the state in units of the new shift, and, where references jump, 2^64 lower
-            // (one factor could lie below fp32's range)
-            const int jump = all - all0 > 70 ? 64 : 0;
-            if (BF16 && (shift != shift0 || jump != 0)) {
-              const float fo = kv4::two_to(max(shift0 - shift - jump, -126)), fl = kv4::two_to(-jump);
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  l[nb][j] *= fl;
-                  r[nb][j] += static_cast<float>(jump);
-#pragma unroll
-                  for (int t = 0; t < kT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                      o[t][i][nb][j] *= fo;
-                      o[t][i][nb][2 + j] *= fo;
-                    }
-                }
-            }
-            if (BF16 && shift != 0) {
+              for (int j = 0; j < 2; ++j)
+                stop |= fabsf(mx[nb][j]) >= 0x1p22f && mx[nb][j] != -INFINITY;
+            if (parted && vmax >= 2.0f * v_lim) {
+              // keys that not all columns see, with scales four times all that they do
+              float all = 0.f;
 #pragma unroll
               for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-#pragma unroll
-                  for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = kv4::move2(vsc[mb][h][i], -shift);
+                  if (key0 + 16 * mb + 8 * h + key_g < max(min_lim, key0 + 1))
+                    all = fmaxf(all, row_scale(vsc[mb][h]));
+              stop |= vmax >= 4.0f * kv4::max_over_rows(all);
             }
-            __syncwarp();
-            if (lane == 0) v_power[warp] = top, v_moved[warp] = shift;
-            // (negative: every tile from here to the unit's end)
-            v_lim = parted || shift != 0 ? -1.0f : top == kv4::kVNone ? kv4::kVZeros : kv4::two_to(top + 1);
-          } else {
+            if (__any_sync(0xffffffffu, stop)) return false;
             v_lim = kv4::two_to(power + 1);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(power);
+          } else {
+            constexpr int kLow = kv4::kVLow<BF16>;
+            bool large = far.against;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) large |= fabsf(mx[nb][j]) >= 0x1p22f && mx[nb][j] != -INFINITY;
+            const bool was_against = far.against, against = __any_sync(0xffffffffu, large);
+            const int top0 = far.top, shift0 = far.shift;
+            const int top = max(top0, kv4::power_of(vmax));
+            // (against: probabilities are at most one, V's scales are moved to near 2^5, or
+            // as near as one factor of the type takes them)
+            const int shift = against ? (top == kv4::kVNone ? 0 : BF16 ? max(top - 5, -126) : min(max(top - 5, -15), 11))
+                                      : BF16 ? kv4::v_shift(top) : 0;
+            const int all0 = max(top0 - shift0, kLow), all = against ? 5 : max(top - shift, kLow);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(all);
+            if (against) {
+              // Scores, and what is there already, against the largest score (before
+              // cs) first of all.
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const bool first = mv[nb][j] == -INFINITY;
+                  const float before =
+                      first ? -INFINITY : was_against ? far.raw[nb][j] : __fdividef(mv[nb][j] - 8.0f, cs[nb][j]);
+                  const float t = fmaxf(before, kv4::max_over_rows(fmaxf(fmaxf(s[0][nb][j], s[0][nb][2 + j]),
+                                                                         fmaxf(s[1][nb][j], s[1][nb][2 + j]))));
+                  far.raw[nb][j] = t;
+                  if (t != -INFINITY) {
+                    if (!first) {
+                      r[nb][j] = was_against ? (before - t) * cs[nb][j] : fmaf(-t, cs[nb][j], r[nb][j]);
+                      mv[nb][j] = 8.0f;
+                    }
+                    mx[nb][j] = -INFINITY;
+#pragma unroll
+                    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                      for (int h = 0; h < 2; ++h) {
+                        s[mb][nb][2 * h + j] -= t;
+                        mx[nb][j] = fmaxf(mx[nb][j], cs[nb][j] * s[mb][nb][2 * h + j]);
+                      }
+                  }
+                }
+            } else if (parted) {
+              // Not all columns see all of the tile's keys: each goes by the scales that
+              // it does see, so that a later token's cost an earlier query no bits, and
+              // keeps its reference once its keys have ended.
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  float seen = 0.f;
+#pragma unroll
+                  for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                      if (key0 + 16 * mb + 8 * h + key_g < lim[nb][j]) seen = fmaxf(seen, row_scale(vsc[mb][h]));
+                  seen = kv4::max_over_rows(seen);
+                  if (lim[nb][j] <= key0)
+                    lg[nb][j] = r[nb][j] - (mv[nb][j] - 8.0f) + 5.0f;
+                  else if (lim[nb][j] < key0 + kAttnKeys)
+                    lg[nb][j] = static_cast<float>(max(max(top0, kv4::power_of(seen)) - shift, kLow));
+                }
+            }
+            // the state in units of the new shift, and, where references jump, 2^64 lower
+            // (one factor could lie below fp32's range)
+            const int jump = BF16 && !against && all - all0 > 70 ? 64 : 0;
+            const float fo = kv4::two_to(min(max(shift0 - shift - jump, -126), 126)), fl = kv4::two_to(-jump);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                l[nb][j] *= fl;
+                r[nb][j] += static_cast<float>(jump);
+#pragma unroll
+                for (int t = 0; t < kT; ++t)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    o[t][i][nb][j] *= fo;
+                    o[t][i][nb][2 + j] *= fo;
+                  }
+              }
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = kv4::move2<BF16>(vsc[mb][h][i], -shift);
+            far.top = top, far.shift = shift, far.against = against;
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -944,6 +1000,29 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
             }
           }
         }
+        return true;
+      };
+
+      int it = 0;
+      bool wide = false;
+#pragma unroll 1
+      for (; it < n && !wide; it += !wide) {
+        next_tile();
+        const int key0 = (t0 + it) * kAttnKeys;
+        // (of a tile behind the last key nothing was fetched)
+        wide = key0 < keys && !tile(std::false_type(), key0);
+      }
+      if (wide) {
+        far.top = v_lim == kv4::kVStart ? kv4::kVNone : kv4::exponent(v_lim) - 1;
+        far.shift = 0;
+        far.against = false;
+#pragma unroll 1
+        for (;;) {
+          const int key0 = (t0 + it) * kAttnKeys;
+          if (key0 < keys) tile(std::true_type(), key0);
+          if (++it == n) break;
+          next_tile();
+        }
       }
 
       // ---- the unit's end: to the outputs, or a partial state ----
@@ -958,20 +1037,21 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           parts[2 * warp + (head ? 0 : 1)] = {unit_first, cur, part};
       }
       __syncwarp();
-      // References of states that are joined lie within 2^70 of one another (as far
-      // as their scores do: a weight below 2^-126 is lost), and sums of V, not yet
-      // divided, within fp32: so a state's unit is the V scales' between 2^-30 and
-      // 2^40, else the nearer end.
-      if (BF16 && (v_lim < 0x1p-29f || v_lim > 0x1p41f)) {
-        const int shift = v_lim < 0.f ? v_moved[warp] : 0;
+      if (wide) {
+        // Its unit is the V scales' within kVPlain, else the nearer end.
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // the power in the column's reference
-            const int lg = mv[nb][j] == -INFINITY ? 0 : __float2int_rn(r[nb][j] - mv[nb][j] + 13.0f);
-            const int unit = min(max(lg + shift, -30), 40);
-            const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
+            int lg = mv[nb][j] == -INFINITY ? 0 : __float2int_rn(r[nb][j] - mv[nb][j] + 13.0f);
+            int unit = min(max(lg + far.shift, kv4::kVPlainLow), kv4::kVPlainHigh);
+            if (far.against) {
+              // (the same for all, so that equal scores of two states weigh the same)
+              lg = 5, unit = far.shift > 80 ? kv4::kVPlainHigh : 5;
+              r[nb][j] = far.raw[nb][j] * cs[nb][j];
+            }
+            const float to_o = kv4::two_to(lg + far.shift - unit), to_l = kv4::two_to(lg - unit);
             l[nb][j] *= to_l;
             r[nb][j] += static_cast<float>(unit - lg);
 #pragma unroll

@@ -643,11 +643,13 @@ int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
  * position seq_len[s] - n + i, attending to the positions up to its own.
  *   O = softmax(scale * q . K^T) V over the values the codes stand for;
  *   scores, softmax and O's sums in fp32 (the codes are exact operands of the
- *   matrix products, q is used to at least 11 bits below its row's largest
+ *   matrix products, q is used to 11 bits or 2^-26 of its row's largest
  *   magnitude, each probability times its V scale is rounded once to 11 bits, or
- *   to 2^-30 of the largest V scale met where that is coarser), O rounded once
- *   to the cache's type.  A row that is not finite reaches the queries that
- *   attend to it, and no others.
+ *   where that is coarser to 2^-30 of the largest V scale that the query attends
+ *   to, 2^-26 if later tokens of the same call have larger ones), O rounded once
+ *   to the cache's type.  All that append writes is in range, up to scores of
+ *   2^127; scores from about 2^22 on differ by no less than fp32's last bit.  A
+ *   row that is not finite reaches the queries that attend to it, and no others.
  * A query with no position to attend to gets O = 0 and an LSE of -infinity.  A
  * sequence with no queries reads nothing.  A table entry that names no page is
  * reported by tilemix_get_error() as INVALID_ARG; what its sequence gets is then

@@ -207,3 +207,52 @@ def test_scores_that_differ_by_their_last_bits(dtype, power, rising):
             v = pool.row("v", s)[:n - (start[s + 1] - i) + 1, 0]
             slack = 2.0 ** -6 * np.abs(v).max()    # bf16's rounding, P s_v's and the sums'
             assert (o[i] >= v.min(axis=0) - slack).all() and (o[i] <= v.max(axis=0) + slack).all()
+
+
+@pytest.mark.parametrize("d,group,rep,queries", SHAPES)
+@pytest.mark.parametrize("power", [-126, -110, -70, 70, 100, 104, 112, 120, 125])
+def test_keys_of_one_magnitude(d, group, rep, queries, power):
+    """All of K near one power of two, with queries that bring the scores back to
+    ordinary ones."""
+    pool = kc.Pool(np.random.default_rng(9), [40, 1500], 2, d, group, 32, "bf16")
+    _fill(pool, "k", lambda at, n: np.full(n, 2.0 ** power))
+    _check(pool, queries, 2 * rep, q_scale=2.0 ** -min(max(power, -124), 124))
+
+
+@pytest.mark.parametrize("d,group,rep,queries", SHAPES)
+def test_keys_of_many_magnitudes(d, group, rep, queries):
+    """K from 2^-100 to 2^100 along a sequence."""
+    pool = kc.Pool(np.random.default_rng(10), [200, 1900], 2, d, group, 32, "bf16")
+    _fill(pool, "k", lambda at, n: 2.0 ** (at * 200 // n - 100.0))
+    _check(pool, queries, 2 * rep, q_scale=2.0 ** -99)
+
+
+@pytest.mark.parametrize("d,group,rep,queries", SHAPES)
+@pytest.mark.parametrize("power", [90, 104, 116, 122])
+def test_one_key_takes_all(d, group, rep, queries, power):
+    """Keys so large that the largest score takes all: O is its row of V, wherever
+    the next score is further away than the scores' rounding."""
+    rng = np.random.default_rng(11)
+    pool = kc.Pool(rng, [33, 700], 2, d, group, 32, "bf16")
+    _fill(pool, "k", lambda at, n: np.full(n, 2.0 ** power))
+    start = np.concatenate([[0], np.cumsum(queries)])
+    q = kc.draw(rng, (int(start[-1]), 2 * rep, d), "bf16")
+    o = pool.cache().attend(kc.to_device(q, "bf16"), 700, max_new=max(queries),
+                            token_start=torch.tensor(start.tolist(), dtype=torch.int32, device="cuda"))
+    o = kc.to_numpy(o)
+    assert np.isfinite(o).all()
+    sure = 0
+    for s, n in enumerate(pool.lengths):
+        k, v = pool.row("k", s), pool.row("v", s)
+        for i in range(start[s], start[s + 1]):
+            m = n - (start[s + 1] - i) + 1
+            for h in range(2 * rep):
+                x = k[:m, h // rep] @ q[i, h]
+                first, second = np.argsort(x)[::-1][:2]
+                reach = np.abs(q[i, h]).sum() * np.abs(k[:m, h // rep]).max()
+                if x[first] - x[second] > 2.0 ** -16 * reach:
+                    sure += 1
+                    # the value itself, rounded; P s_v to 11 bits
+                    assert (np.abs(o[i, h] - v[first, h // rep]) <=
+                            (kc.EPS["bf16"] + 2.0 ** -10) * np.abs(v[first, h // rep])).all()
+    assert sure > 0

@@ -33,7 +33,9 @@
 //     transposition, but needs registers for zero rows: 390 us for 256.)
 // Q is scaled per column by a power of two, so its largest magnitude is near
 // 2^14 and every channel keeps at least 11 bits (fp16 has 5 of exponent,
-// bf16 has 8) down to 2^-28 of it.  K's scales multiply the scores, V's the
+// bf16 has 8) down to 2^-28 of it.  In bf16, whose K scales reach 2^125, K's
+// codes enter as 2^-10 of themselves and Q's largest is near 2 (its 8 bits kept
+// down to 2^-17 of it), so that no score before its factor passes fp32.  K's scales multiply the scores, V's the
 // probabilities: P s_v is what is rounded to fp16 (11 bits).  A column's
 // probabilities are 2^(score - r) with r = the largest score + log2 of the largest V scale (its
 // power of two) - 5, so P s_v stays near 2^5 at the top, and r moves only when
@@ -123,6 +125,22 @@ __device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)
       "{%8, %9}, {%10, %10, %10, %10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// K's codes, in bf16 2^-10 of them.
+template <bool DOWN>
+__device__ __forceinline__ uint32_t k_low(uint32_t x) {
+  if constexpr (!DOWN) return code_low(x);
+  uint32_t y = or_1024(x, 0x000F000Fu);  // (1024 + u) 2^-10 - (1 + 2^-7)
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x14001400u), "r"(0xBC08BC08u));
+  return y;
+}
+template <bool DOWN>
+__device__ __forceinline__ uint32_t k_high(uint32_t x) {
+  if constexpr (!DOWN) return code_high(x);
+  uint32_t y = or_1024(x, 0x00F000F0u);  // (1024 + 16 u) 2^-14 - (2^-4 + 2^-7)
+  asm("fma.rn.f16x2 %0, %0, %1, %2;" : "+r"(y) : "r"(0x04000400u), "r"(0xAC80AC80u));
+  return y;
 }
 
 // Larger magnitude-ordered half of two packed non-negative values (NaNs drop out).
@@ -589,9 +607,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         }
         am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
         am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-        // f = 2^(14 - exponent of the largest magnitude), 1 for zeros, infinities, NaN
+        // f = 2^(14 - exponent of the largest magnitude) (bf16: 2^(1 - exponent), but
+        // from 2^61 on, where the score's factor would pass fp32), 1 for zeros,
+        // infinities, NaN
         const uint32_t ex = __float_as_uint(kv4::unpack1<BF16>(am)) >> 23;
-        const uint32_t fe = (am == 0 || am >= kv4::kInfBits<BF16>) ? 127u : min(268u - ex, 253u);
+        const uint32_t fe = (am == 0 || am >= kv4::kInfBits<BF16>) ? 127u
+                            : min((BF16 && ex < 188u ? 255u : 268u) - ex, 253u);
         const float f = __uint_as_float(fe << 23);
         const float inv_f = __uint_as_float((254u - fe) << 23);
 #pragma unroll
@@ -603,7 +624,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           qf[nb][t][2] = kv4::pack2<false>(c01.y * f, c45.y * f);
           qf[nb][t][3] = kv4::pack2<false>(c23.y * f, c67.y * f);
         }
-        const float unit = inv_f * p.scale_log2;
+        const float unit = (BF16 ? inv_f * 0x1p10f : inv_f) * p.scale_log2;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int from = (2 * q4 + j) * 4;  // a lane of that column
@@ -619,7 +640,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
       // that moves it, their sum; per unit: the V scale that moves it
       float r[NB][2], mv[NB][2], l[NB][2];
       float v_lim = kv4::kVStart;
-      Beyond<NB> far;
+      Beyond<NB> far = {};
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -693,10 +714,10 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
 #pragma unroll
             for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
               const uint32_t x = k0[t], y = k1[t], xh = x >> 8, yh = y >> 8;
-              const uint32_t ev[4] = {kv4::code_low(x), kv4::code_low(y), kv4::code_low(xh),
-                                      kv4::code_low(yh)};
-              const uint32_t od[4] = {kv4::code_high(x), kv4::code_high(y), kv4::code_high(xh),
-                                      kv4::code_high(yh)};
+              const uint32_t ev[4] = {kv4::k_low<BF16>(x), kv4::k_low<BF16>(y), kv4::k_low<BF16>(xh),
+                                      kv4::k_low<BF16>(yh)};
+              const uint32_t od[4] = {kv4::k_high<BF16>(x), kv4::k_high<BF16>(y), kv4::k_high<BF16>(xh),
+                                      kv4::k_high<BF16>(yh)};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 if (t == i * kTg)

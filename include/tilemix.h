@@ -650,7 +650,10 @@ int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
  *   to the cache's type.  All that append writes is in range, up to scores of
  *   2^127; scores from about 2^22 on differ by no less than fp32's last bit.  A
  *   row that is not finite reaches the queries that attend to it, and no others.
- * A query with no position to attend to gets O = 0 and an LSE of -infinity.  A
+ * A query with no position to attend to gets O = 0 and an LSE of -infinity, and
+ * so does every query of a sequence with granted[s] = 0: the plan refused its
+ * tokens, so seq_len[s] does not count them, and without `granted` its queries
+ * would be taken for its last tokens, which are others.  A
  * sequence with no queries reads nothing.  A table entry that names no page is
  * reported by tilemix_get_error() as INVALID_ARG; what its sequence gets is then
  * meaningless.  Rows of q and o at and behind
@@ -683,6 +686,7 @@ typedef struct tilemix_kv4_attn_args {
                                  that uses it; every call leaves it zero.  Calls that may
                                  run at the same time need a workspace and a sync array
                                  each */
+  const int32_t* granted;     /* device [nseq] as tilemix_page_plan left it, or NULL: all are */
 } tilemix_kv4_attn_args;
 
 /* Bytes of workspace (partial softmax states; about 12 MB on a B200, whatever the batch). */

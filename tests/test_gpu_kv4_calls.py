@@ -1,0 +1,113 @@
+"""GPU tests of how the 4-bit cache's calls go together: refused tokens, tables,
+streams and sizes, each against the oracle."""
+import numpy as np
+import pytest
+
+from oracle import kv4 as okv
+
+torch = pytest.importorskip("torch")
+from tests import kv4_cases as kc  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+@pytest.fixture(autouse=True)
+def _status():
+    yield
+    import tile_routed_mixed_b200 as tm
+    assert tm.tilemix_get_error() == tm.OK
+
+
+def _i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+# -------------------------------------------------------- refused tokens ---
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("graph", [False, True])
+def test_a_step_that_is_refused(dtype, graph):
+    """Steps through plan, append and attend in a pool that runs out and with rows
+    that are full: the queries of refused sequences get zeros and an LSE of
+    -infinity, all others what the oracle says; a later step goes on from there."""
+    import tile_routed_mixed_b200 as tm
+    rng = np.random.default_rng(40)
+    hq, hk, d, page, group = 6, 2, 64, 16, 32
+    cache = tm.TileMixKV4Cache(9, page, hk, d, 4, 3, group=group, dtype=kc.TORCH[dtype])
+    want = okv.Pages(9, page, 4, 3)
+    coded = lambda x: okv.values(*okv.quantise(x, group, dtype), group)
+    hist = [[np.zeros((0, hk, d))] * 2 for _ in range(4)]
+    # pages of 16, three a row, nine in all: 2 + 1 + 3 + 2; sequence 2 is full, one page
+    # is left for two that need one; then sequence 2 ends and all fit
+    steps = [[30, 16, 48, 20], [1, 1, 1, 13], [17, 2, 0, 1], [1, 16, -48, 1], [2, 17, 33, 0]]
+    top = max(sum(max(x, 0) for x in st) for st in steps)
+    new, out = _i32([0] * 4), cache.new_plan(top)
+    q, k, v = (torch.zeros((top, h, d), dtype=kc.TORCH[dtype], device="cuda") for h in (hq, hk, hk))
+    o, lse = torch.zeros_like(q), torch.zeros((hq, top), device="cuda")
+
+    def step():
+        cache.plan(new, out=out)
+        cache.append(k, v, out.slots)
+        cache.attend(q, 48, token_start=out.token_start, max_new=48, out=o, lse=lse, granted=out.granted)
+
+    run = step
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        run = g.replay
+    refused = 0
+    for st in steps:
+        qh, kh, vh = (kc.draw(rng, (top, h, d), dtype) for h in (hq, hk, hk))
+        for t, x in ((q, qh), (k, kh), (v, vh)):
+            t.copy_(kc.to_device(x, dtype))
+        new.copy_(_i32(st))
+        o.fill_(7.0)
+        lse.fill_(7.0)
+        run()
+        start, _, granted = want.plan(st, top)
+        assert out.granted.tolist() == granted and out.token_start.tolist() == start
+        got, gl = kc.to_numpy(o), kc.to_numpy(lse)
+        for s, m in enumerate(st):
+            a, b = start[s], start[s + 1]
+            if not granted[s]:
+                refused += 1
+                assert not got[a:b].any() and np.isneginf(gl[:, a:b]).all()
+                continue
+            hist[s] = [x[:max(0, len(x) + m)] for x in hist[s]] if m < 0 else \
+                [np.concatenate([x, coded(y[a:b])]) for x, y in zip(hist[s], (kh, vh))]
+        pool = type("P", (), {"dtype": dtype})
+        live = [s for s in range(4) if granted[s]]
+        for s in live:
+            kc.check_attend(got[start[s]:start[s + 1]], gl[:, start[s]:start[s + 1]], qh[start[s]:start[s + 1]], pool,
+                            [len(hist[s][0])], [0, start[s + 1] - start[s]], hq, kv=lambda _: hist[s])
+        assert (got[start[-1]:] == 7.0).all() and (gl[:, start[-1]:] == 7.0).all()
+        assert cache.seq_len.tolist() == [len(x[0]) for x in hist]
+    assert refused >= 3
+    bad = _i32([1] * 3)
+    with pytest.raises(ValueError):
+        cache.attend(q[:4], 48, granted=bad)
+
+
+def test_refused_among_many_and_long():
+    """Granted or not over units that several CTAs share, one query per sequence."""
+    rng = np.random.default_rng(41)
+    lengths = [int(x) for x in rng.integers(1, 3000, 24)]
+    pool = kc.Pool(rng, lengths, 2, 64, 64, 64, "bf16")
+    q = kc.draw(rng, (24, 4, 64), "bf16")
+    granted = [int(x) for x in rng.integers(0, 2, 24)]
+    o, lse = pool.cache().attend(kc.to_device(q, "bf16"), 3000, lse=True, granted=_i32(granted))
+    o, lse = kc.to_numpy(o), kc.to_numpy(lse)
+    for s in range(24):
+        if granted[s]:
+            one = type("P", (), {"dtype": "bf16"})
+            kc.check_attend(o[s:s + 1], lse[:, s:s + 1], q[s:s + 1], one, [lengths[s]], [0, 1], 4,
+                            kv=lambda _: (pool.row("k", s), pool.row("v", s)))
+        else:
+            assert not o[s].any() and np.isneginf(lse[:, s]).all()

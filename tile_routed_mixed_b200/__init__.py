@@ -155,6 +155,7 @@ class KV4AttnArgs(ctypes.Structure):
         ("max_seqlen", ctypes.c_int), ("max_pages", ctypes.c_int), ("hq", ctypes.c_int),
         ("softmax_scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t), ("sync", ctypes.c_void_p),
+        ("granted", ctypes.c_void_p),
     ]
 
 

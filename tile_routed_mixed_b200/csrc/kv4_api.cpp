@@ -218,6 +218,7 @@ TILEMIX_API int tilemix_kv4_attn(const tilemix_kv4_attn_args* a, void* stream) {
   p.token_start = a->token_start;
   p.seq_len = a->seq_len;
   p.block_table = a->block_table;
+  p.granted = a->granted;
   p.heads = reinterpret_cast<float*>(ws + w.heads);
   p.parts = reinterpret_cast<float*>(ws + w.parts);
   p.sync = a->sync;

@@ -57,6 +57,7 @@ struct Kv4AttnParams {
   const int32_t* token_start;
   const int32_t* seq_len;
   const int32_t* block_table;
+  const int32_t* granted;  // or nullptr
   float* heads;        // workspace: partial states that a warp finishes mid-range
   float* parts;        // workspace: partial states of CTAs, two per CTA
   unsigned int* sync;  // arrivals of the CTAs that share a unit, by the unit's first CTA

@@ -223,6 +223,7 @@ __device__ __forceinline__ SeqWork seq_work(const Kv4AttnParams& p, int s) {
   const int top = static_cast<int>(
       min(static_cast<long long>(p.max_pages) << p.pool.page_shift, 0x7fffff00LL));
   w.len = min(max(__ldg(p.seq_len + s), 0), top);
+  if (p.granted && __ldg(p.granted + s) == 0) w.len = 0;  // its queries have no rows
   w.row0 = s;
   w.queries = 1;
   if (p.token_start) {

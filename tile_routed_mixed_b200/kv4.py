@@ -6,9 +6,12 @@ stack (all on the device), and the attention's workspaces.  A step is
 
     plan = cache.plan(new_len, max_tokens=n)      # pages and slots
     cache.append(k, v, plan.slots)                # rows in, 4 bits
-    o = cache.attend(q, max_seqlen, token_start=plan.token_start, max_new=m)
+    o = cache.attend(q, max_seqlen, token_start=plan.token_start, max_new=m,
+                     granted=plan.granted)
 
-and none of it reads anything back to the host.
+and none of it reads anything back to the host.  A sequence that the plan refuses
+(plan.granted 0: no pages, or no room in its row) stays as it was, and its queries
+get O = 0 and an LSE of -infinity.
 """
 from __future__ import annotations
 
@@ -248,17 +251,19 @@ class TileMixKV4Cache:
         return tuple(out)
 
     def attend(self, q, max_seqlen, token_start=None, max_new=1, softmax_scale=0.0, out=None,
-               lse=False, stream=None):
+               lse=False, stream=None, granted=None):
         """Attention of the newest tokens over the cache (see tilemix_kv4_attn).
         q [rows, hq, d]: sequence s's queries are rows token_start[s] ..
         token_start[s + 1] - 1 (int32 [nseq + 1]), or row s if token_start is
         None.  max_seqlen and max_new bound the lengths and the queries per
-        sequence.  Returns o like q, or (o, LSE [hq, rows]) if lse; `out` and a
+        sequence.  granted: the plan's (int32 [nseq]); a step whose plan may refuse
+        tokens has to pass it, as a refused sequence's queries stand for tokens that
+        are not in the cache.  Returns o like q, or (o, LSE [hq, rows]) if lse; `out` and a
         tensor as `lse` are written in place.  Rows that no sequence covers are
         not written (in a new tensor they hold nothing meaningful)."""
         if stream is not None or _device_now() != self._index:
             return self._elsewhere(stream, self.attend, q, max_seqlen, token_start, max_new,
-                                   softmax_scale, out, lse)
+                                   softmax_scale, out, lse, None, granted)
         shape = q.shape
         if not (q.dtype is self.dtype and q.get_device() == self._index and len(shape) == 3
                 and shape[2] == self.d and q.is_contiguous()):
@@ -272,6 +277,8 @@ class TileMixKV4Cache:
                 raise ValueError("q: the cache holds %d sequences" % self.max_seqs)
         else:
             n, start = self._vector(token_start, "token_start", 1), token_start.data_ptr()
+        if granted is not None:
+            self._expect(granted, _i32, (n,), "granted")
         if out is None:
             out = torch.empty_like(q)
         else:
@@ -286,6 +293,7 @@ class TileMixKV4Cache:
         with self._lock:
             a.q, a.o, a.token_start = q.data_ptr(), out.data_ptr(), start
             a.lse = None if lse is None else lse.data_ptr()
+            a.granted = None if granted is None else granted.data_ptr()
             a.nseq, a.total_q, a.hq = n, rows, hq
             a.max_new, a.max_seqlen, a.softmax_scale = max_new, max_seqlen, softmax_scale
             if rows and n:

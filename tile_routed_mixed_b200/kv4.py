@@ -39,6 +39,12 @@ _capturing = torch._C._cuda_isCurrentStreamCapturing
 _i32 = torch.int32
 
 
+def _held(name):
+    """A tensor of the object, to be written in place: the calls' argument blocks hold
+    its address, so another one cannot take its place."""
+    return property(lambda self: self._tensors[name])
+
+
 def _dtype_id(dtype):
     names = {torch.float16: "fp16", torch.bfloat16: "bf16"}
     if dtype not in names:
@@ -56,12 +62,18 @@ class TileMixKV4Cache:
     tables   (block_table [max_seqs, max_pages], seq_len [max_seqs],
              free_list [num_pages], free_count [1]), int32, likewise
 
+    The tensors (k_codes, k_scale, v_codes, v_scale, block_table, seq_len,
+    free_list, free_count) are the object's for good: write them in place.
+
     The object belongs to one device, whichever is current; `stream` picks the
     stream of a call (default: the current one of that device).  Two calls that
     change the same tables or rows, or read what another writes, must be ordered
     by the caller, as for any tensor.  attend() keeps a workspace per stream, so
     calls on different streams may run at the same time; a call that is being
     captured into a CUDA graph takes one from the graph's own memory."""
+
+    _names = ("k_codes", "k_scale", "v_codes", "v_scale", "block_table", "seq_len", "free_list", "free_count")
+    (k_codes, k_scale, v_codes, v_scale, block_table, seq_len, free_list, free_count) = map(_held, _names)
 
     def __init__(self, num_pages, page_size, hk, d, max_seqs, max_pages, group=32,
                  dtype=torch.float16, device="cuda", pool=None, tables=None):
@@ -97,8 +109,7 @@ class TileMixKV4Cache:
                       torch.full((1,), self.num_pages, dtype=_i32, device=dev))
         for x, (s, t) in zip(tables, shapes, strict=True):
             self._expect(x, t, s, "tables")
-        self.k_codes, self.k_scale, self.v_codes, self.v_scale = pool
-        self.block_table, self.seq_len, self.free_list, self.free_count = tables
+        self._tensors = dict(zip(self._names, (*pool, *tables)))
         c = KV4Cache()
         c.k_codes, c.k_scale = self.k_codes.data_ptr(), self.k_scale.data_ptr()
         c.v_codes, c.v_scale = self.v_codes.data_ptr(), self.v_scale.data_ptr()

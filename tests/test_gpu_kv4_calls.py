@@ -111,3 +111,39 @@ def test_refused_among_many_and_long():
                             kv=lambda _: (pool.row("k", s), pool.row("v", s)))
         else:
             assert not o[s].any() and np.isneginf(lse[:, s]).all()
+
+
+# --------------------------------------------------------------- streams ---
+
+def test_tensors_dropped_after_a_call_on_another_stream():
+    """q, token_start and the appended rows are dropped and their sizes allocated and
+    filled again while the side stream has not begun: results are those of the
+    first contents."""
+    rng = np.random.default_rng(42)
+    pool = kc.Pool(rng, [500, 90], 2, 128, 32, 16, "fp16")
+    cache = pool.cache()
+    side = torch.cuda.Stream()
+    out = torch.empty((3, 4, 128), dtype=torch.float16, device="cuda")
+    k2, v2 = (torch.empty((590, 2, 128), dtype=torch.float16, device="cuda") for _ in range(2))
+    q, k, v = (kc.draw(rng, (3, h, 128), "fp16") for h in (4, 2, 2))
+    slots = [int(pool.table[0, 499 // 16]) * 16 + 499 % 16] + [int(pool.table[1, p // 16]) * 16 + p % 16 for p in (88, 89)]
+    tensors = [kc.to_device(x, "fp16") for x in (q, k, v)] + [_i32(slots), _i32([0, 1, 3]), _i32([0, 500])]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+    cache.append(tensors[1], tensors[2], tensors[3], stream=side)
+    cache.attend(tensors[0], 500, token_start=tensors[4], max_new=2, out=out, stream=side)
+    cache.gather(tensors[5], 590, out=(k2, v2), stream=side)
+    shapes = [(x.shape, x.dtype) for x in tensors]
+    del tensors
+    for _ in range(4):  # (garbage that is legal as slots, offsets and values)
+        junk = [torch.zeros(s, dtype=t, device="cuda") for s, t in shapes]
+    torch.cuda.synchronize()
+    del junk
+    coded = lambda x: okv.values(*okv.quantise(x, 32, "fp16"), 32)
+    hist = []
+    for s, (a, b) in enumerate(((0, 1), (1, 3))):
+        hist.append([np.concatenate([pool.row(w, s)[:-(b - a)], coded(x[a:b])]) for w, x in (("k", k), ("v", v))])
+    kc.check_attend(kc.to_numpy(out), None, q, pool, [500, 90], [0, 1, 3], 4, kv=lambda s: hist[s])
+    for t, i in ((k2, 0), (v2, 1)):
+        assert np.array_equal(kc.to_numpy(t), okv.round_to(np.concatenate([h[i] for h in hist]), "fp16"))

@@ -31,3 +31,50 @@ def test_the_tensors_cannot_be_rebound(name):
     with pytest.raises(AttributeError):
         setattr(c, name, torch.ones(3))
     assert getattr(c, name) is x
+
+
+class _Tensor:
+    """Stands for a tensor on a device: notes the streams that hold its memory."""
+    is_cuda = True
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+class _Stream:
+    def __init__(self, handle, device):
+        self.cuda_stream, self.device = handle, device
+
+
+def test_a_call_on_another_stream_holds_its_tensors(monkeypatch):
+    """A tensor that the caller drops right after a call on another stream must not
+    be handed out again while that stream still reads it; the same for the
+    cache's own when the cache goes."""
+    import contextlib
+
+    import tile_routed_mixed_b200.kv4 as kv4
+    entered = []
+
+    @contextlib.contextmanager
+    def on(stream):
+        entered.append(stream)
+        yield
+
+    monkeypatch.setattr(kv4.torch.cuda, "stream", on)
+    own, dev = [_Tensor() for _ in NAMES], torch.device("cuda", 0)
+    c = _bare(_tensors=dict(zip(NAMES, own)), _held_on=set(), device=dev, _index=0)
+    q, plan, host = _Tensor(), kv4.PagePlan(_Tensor(), _Tensor(), _Tensor()), torch.zeros(2)
+    streams = [_Stream(11, dev), _Stream(12, dev)]
+    for s in (streams[0], streams[1], streams[0]):
+        assert c._elsewhere(s, lambda *a: a, q, None, 7, plan, host, True) == (q, None, 7, plan, host, True)
+    assert entered == [streams[0], streams[1], streams[0]]
+    for x in (q, *plan):
+        assert x.streams == [streams[0], streams[1], streams[0]]
+    for x in own:
+        assert x.streams == streams
+    with pytest.raises(ValueError):
+        c._elsewhere(_Stream(13, torch.device("cuda", 1)), lambda *a: a, q)
+    assert len(q.streams) == 3

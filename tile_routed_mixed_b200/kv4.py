@@ -66,7 +66,10 @@ class TileMixKV4Cache:
     free_list, free_count) are the object's for good: write them in place.
 
     The object belongs to one device, whichever is current; `stream` picks the
-    stream of a call (default: the current one of that device).  Two calls that
+    stream of a call (default: the current one of that device).  A call with
+    `stream` holds the memory of its tensors until that stream is done with them
+    (they may be dropped after the call); new tensors that it returns belong to that
+    stream, which another has to wait for.  Two calls that
     change the same tables or rows, or read what another writes, must be ordered
     by the caller, as for any tensor.  attend() keeps a workspace per stream, so
     calls on different streams may run at the same time; a call that is being
@@ -135,6 +138,7 @@ class TileMixKV4Cache:
         }
         self._lock = threading.Lock()  # on the blocks: a call fills one and enqueues it
         self._spaces = {}
+        self._held_on = set()  # streams, by handle, that _tensors are recorded on
         self._f32 = torch.empty(0, dtype=torch.float32, device=dev)
 
     # ---------------------------------------------------------------- checks
@@ -167,8 +171,21 @@ class TileMixKV4Cache:
                 return fn(*args)
         if stream.device != self.device:
             raise ValueError("the stream belongs to %s, the cache to %s" % (stream.device, self.device))
+        self._hold(stream, args)
+        if stream.cuda_stream not in self._held_on:  # (for as long as they live)
+            self._hold(stream, self._tensors.values())
+            self._held_on.add(stream.cuda_stream)
         with torch.cuda.stream(stream):
             return fn(*args)
+
+    def _hold(self, stream, args):
+        """Tensors among args, dropped by the caller after the call, are not handed out
+        again before `stream` is done with them."""
+        for x in args:
+            if isinstance(x, (tuple, list)):
+                self._hold(stream, x)
+            elif getattr(x, "is_cuda", False):
+                x.record_stream(stream)
 
     def _call(self, name):
         fn, args = self._calls[name]

@@ -78,3 +78,16 @@ def test_a_call_on_another_stream_holds_its_tensors(monkeypatch):
     with pytest.raises(ValueError):
         c._elsewhere(_Stream(13, torch.device("cuda", 1)), lambda *a: a, q)
     assert len(q.streams) == 3
+
+
+@pytest.mark.parametrize("over", [
+    dict(page_size=24), dict(page_size=8), dict(page_size=2048), dict(page_size=0), dict(num_pages=1 << 27),
+    dict(num_pages=0), dict(hk=0), dict(hk=1 << 15), dict(max_seqs=1 << 20, max_pages=1 << 12), dict(max_pages=0),
+    dict(d=96), dict(group=16), dict(d=64, group=128), dict(dtype=torch.float32)], ids=str)
+def test_the_constructor_refuses_what_the_calls_would(over):
+    """Before anything is allocated."""
+    import tile_routed_mixed_b200 as tm
+    args = dict(num_pages=8, page_size=16, hk=2, d=128, max_seqs=2, max_pages=4, group=32, dtype=torch.float16)
+    args.update(over)
+    with pytest.raises(ValueError):
+        tm.TileMixKV4Cache(**args)

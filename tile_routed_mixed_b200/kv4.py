@@ -85,6 +85,7 @@ class TileMixKV4Cache:
         self.hk, self.d, self.group = int(hk), int(d), int(group)
         self.max_seqs, self.max_pages = int(max_seqs), int(max_pages)
         self.dtype = dtype
+        dt = _dtype_id(dtype)
         self.device = torch.device(device)
         if self.device.type != "cuda":
             raise ValueError("the cache lives on a CUDA device")
@@ -92,13 +93,17 @@ class TileMixKV4Cache:
             raise ValueError("d is 64 or 128, group 32, 64 or 128 and at most d")
         if min(self.num_pages, self.page_size, self.hk, self.max_seqs, self.max_pages) < 1:
             raise ValueError("sizes start at 1")
+        if self.page_size not in (16, 32, 64, 128, 256, 512, 1024):
+            raise ValueError("page_size is a power of two, 16 to 1024")
+        if self.num_pages * self.page_size >= 1 << 31 or self.max_seqs * self.max_pages >= 1 << 31 or \
+                self.hk > 32767:
+            raise ValueError("num_pages * page_size and max_seqs * max_pages stay below 2^31, hk below 2^15")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
         self._index = self.device.index
         dev = self.device
         rows = (self.num_pages, self.hk, self.page_size)
         shapes = [(rows + (self.d // 2,), torch.uint8), (rows + (self.d // self.group,), dtype)] * 2
-        dt = _dtype_id(dtype)
         if pool is None:
             pool = [torch.zeros(s, dtype=t, device=dev) for s, t in shapes]
         for x, (s, t) in zip(pool, shapes, strict=True):

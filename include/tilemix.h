@@ -532,7 +532,9 @@ int tilemix_mass_probe(const tilemix_mass_args* args, void* stream);
  * matrix products).
  * Sequence s keeps its token at position p in page block_table[s][p / page_size]
  * at row p % page_size; its slot is page * page_size + row.  Pages may be in any
- * order and may be shared by sequences that only read them. */
+ * order, and append, gather and attention may meet a page in several sequences
+ * (a common prefix that all only read).  tilemix_page_plan does not count who
+ * holds a page: see there. */
 enum { TILEMIX_KV_FP16 = 0, TILEMIX_KV_BF16 = 1 };
 typedef struct tilemix_kv4_cache {
   uint8_t* k_codes;           /* device, 16-byte aligned, and so the next three */
@@ -572,6 +574,11 @@ typedef struct tilemix_kv4_cache {
  * of those that fit) do not exceed F + R, or if they need none.  Tokens that are
  * not granted leave their sequence as it was: granted[s] = 0, their slots -1.
  * Everything else has granted[s] = 1.  Slots past the last token are -1.
+ * An entry that goes back is taken for its sequence's own.  A page that two rows
+ * name would go onto the stack once for each and out again to two sequences, and
+ * that is not noticed; so a sequence that shares its first tokens' pages with
+ * another drops no further than to those tokens, and when it ends the caller
+ * clears the rest: its entries to -1 and its length to 0.
  * Integer arithmetic in a fixed order: the same inputs give the same tables.
  * One launch.  Tables that contradict themselves (a length outside
  * [0, max_pages * page_size], a free count outside [0, num_pages], an entry or a

@@ -147,3 +147,57 @@ def test_tensors_dropped_after_a_call_on_another_stream():
     kc.check_attend(kc.to_numpy(out), None, q, pool, [500, 90], [0, 1, 3], 4, kv=lambda s: hist[s])
     for t, i in ((k2, 0), (v2, 1)):
         assert np.array_equal(kc.to_numpy(t), okv.round_to(np.concatenate([h[i] for h in hist]), "fp16"))
+
+
+# ---------------------------------------------------------- shared pages ---
+
+def test_a_shared_prefix_ends_as_documented():
+    """Two requests share two full pages: one drops to them and is cleared by hand,
+    the other goes on reading them, and no later request is given them before it
+    has ended as well."""
+    import tile_routed_mixed_b200 as tm
+    rng = np.random.default_rng(43)
+    hq, hk, d, page, group = 4, 2, 64, 16, 32
+    cache = tm.TileMixKV4Cache(8, page, hk, d, 3, 6, group=group)
+    coded = lambda x: okv.values(*okv.quantise(x, group, "fp16"), group)
+    pool = type("P", (), {"dtype": "fp16"})
+
+    def step(new):
+        n = sum(max(x, 0) for x in new)
+        q, k, v = (kc.draw(rng, (n, h, d), "fp16") for h in (hq, hk, hk))
+        plan = cache.plan(_i32(new), max_tokens=n)
+        assert plan.granted.tolist() == [1] * 3
+        if n:
+            cache.append(kc.to_device(k, "fp16"), kc.to_device(v, "fp16"), plan.slots)
+        at = 0
+        for s, m in enumerate(new):
+            if m > 0:
+                hist[s] = [np.concatenate([x, coded(y[at:at + m])]) for x, y in zip(hist[s], (k, v))]
+                at += m
+            elif m:
+                hist[s] = [x[:len(x) + m] for x in hist[s]]
+        if n:
+            o, lse = cache.attend(kc.to_device(q, "fp16"), 96, token_start=plan.token_start, max_new=max(new),
+                                  lse=True, granted=plan.granted)
+            kc.check_attend(kc.to_numpy(o), kc.to_numpy(lse), q, pool, [len(h[0]) for h in hist],
+                            plan.token_start.tolist(), hq, kv=lambda s: hist[s])
+
+    empty = [np.zeros((0, hk, d))] * 2
+    hist = [empty, empty, empty]
+    step([32, 0, 0])
+    shared = cache.block_table[0, :2].tolist()
+    cache.block_table[1, :2] = cache.block_table[0, :2]
+    cache.seq_len[1] = 32
+    hist[1] = hist[0]
+    step([3, 20, 0])              # both grow into pages of their own
+    step([1, -20, 0])             # the second ends: back to the shared tokens
+    cache.block_table[1] = -1
+    cache.seq_len[1] = 0
+    hist[1] = empty
+    step([1, 0, 70])              # five pages, none of them shared
+    held = cache.block_table[2, :5].tolist()
+    assert len(set(held + shared)) == 7
+    step([1, 0, 1])
+    step([-38, 0, 1])             # the first ends and returns them
+    assert set(shared) <= set(cache.free_list[:int(cache.free_count)].tolist())
+    step([16, 0, 1])

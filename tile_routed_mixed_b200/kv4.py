@@ -62,6 +62,11 @@ class TileMixKV4Cache:
     tables   (block_table [max_seqs, max_pages], seq_len [max_seqs],
              free_list [num_pages], free_count [1]), int32, likewise
 
+    plan() takes the pages that it frees for the sequence's own.  Rows of block_table
+    that name the same pages (a common prefix, full pages that all only read) are
+    right for append, gather and attend; such a sequence drops no further than to
+    the shared tokens, and at its end its row and its length are cleared in place.
+
     The tensors (k_codes, k_scale, v_codes, v_scale, block_table, seq_len,
     free_list, free_count) are the object's for good: write them in place.
 

@@ -85,23 +85,6 @@ constexpr int kAttnMaxCtas = 160;  // at least one per SM (148 on a B200)
 // for 10.5).
 constexpr int kAttnMinTiles = 8;
 
-template <int D, int GROUP, int NB>
-struct AttnTile {
-  static constexpr int kNg = D / GROUP;                 // scales per row
-  static constexpr int kT = D / 32;                     // 32-channel chunks of a row
-  static constexpr int kCodes = kAttnKeys * D / 2;      // bytes of K's (and V's) codes
-  static constexpr int kScales = kAttnKeys * 2 * kNg;   // ... and scales
-  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
-  static constexpr int kOffV = kCodes;
-  static constexpr int kOffKs = 2 * kCodes;
-  static constexpr int kOffVs = 2 * kCodes + kScales;
-  // as many stages as fit beside 4 KB of the kernel's own, at most six
-  static constexpr int kFit = 223 * 1024 / (kAttnWarps<NB> * kBytes);
-  static constexpr int kStages = kFit > 6 ? 6 : kFit;
-  static_assert(kStages >= 3, "ring too short");
-  static_assert(kStages * kBytes >= 8 * NB * (D + 2) * 4, "a partial state fits a warp's ring");
-};
-
 namespace kv4 {
 
 // 16 bytes from global to shared memory; off, a byte offset, is added to both.
@@ -353,6 +336,38 @@ __device__ __forceinline__ void store_column(const Kv4AttnParams& p, const Unit&
 
 }  // namespace kv4
 
+// A CTA's shared memory beside the rings.
+template <int NB>
+struct AttnShared {
+  static constexpr int kWarps = kAttnWarps<NB>;
+  kv4::Unit units_ahead[kWarps][8];  // from the one computed to the one fetched
+  kv4::Part parts[2 * kWarps];
+  const float* state[2 * kWarps];  // the partial states there are, in order
+  kv4::Cut cuts[kWarps];  // each warp's: kept out of the registers meanwhile
+  // first and last CTA of the unit that the CTA's first, and its last, tile is of
+  int holders[2][2];
+  int state_of[2 * kWarps];
+  int last_here[2];  // states to combine, if this CTA is the last to arrive
+};
+
+template <int D, int GROUP, int NB>
+struct AttnTile {
+  static constexpr int kNg = D / GROUP;                 // scales per row
+  static constexpr int kT = D / 32;                     // 32-channel chunks of a row
+  static constexpr int kCodes = kAttnKeys * D / 2;      // bytes of K's (and V's) codes
+  static constexpr int kScales = kAttnKeys * 2 * kNg;   // ... and scales
+  static constexpr int kBytes = 2 * kCodes + 2 * kScales;
+  static constexpr int kOffV = kCodes;
+  static constexpr int kOffKs = 2 * kCodes;
+  static constexpr int kOffVs = 2 * kCodes + kScales;
+  // as many stages as fit beside the kernel's own, at most six
+  static constexpr int kFit = (227 * 1024 - static_cast<int>(sizeof(AttnShared<NB>))) / (kAttnWarps<NB> * kBytes);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static_assert(kStages * kBytes * kAttnWarps<NB> + sizeof(AttnShared<NB>) <= 227 * 1024, "shared memory");
+  static_assert(kStages >= 3, "ring too short");
+  static_assert(kStages * kBytes >= 8 * NB * (D + 2) * 4, "a partial state fits a warp's ring");
+};
+
 // What a warp keeps of a unit beside its state once it is in the wide form.
 template <int NB>
 struct Beyond {
@@ -371,15 +386,15 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
   constexpr int kTg = kT / kNg;  // chunks per scale group
   static_assert(2 * kWarps <= 32, "runs are found with one ballot");
   extern __shared__ __align__(128) uint8_t attn_smem[];
-  __shared__ kv4::Unit units_ahead[kWarps][8];  // from the one computed to the one fetched
+  __shared__ AttnShared<NB> shared;
+  auto& units_ahead = shared.units_ahead;
+  auto& parts = shared.parts;
+  auto& state = shared.state;
+  auto& cuts = shared.cuts;
+  auto& holders = shared.holders;
+  auto& state_of = shared.state_of;
+  auto& last_here = shared.last_here;
   static_assert(kStages < 8, "a tile ahead may be a unit ahead");
-  __shared__ kv4::Part parts[2 * kWarps];
-  __shared__ const float* state[2 * kWarps];  // the partial states there are, in order
-  __shared__ kv4::Cut cuts[kWarps];  // each warp's: kept out of the registers meanwhile
-  // first and last CTA of the unit that the CTA's first, and its last, tile is of
-  __shared__ int holders[2][2];
-  __shared__ int state_of[2 * kWarps];
-  __shared__ int last_here[2];  // states to combine, if this CTA is the last to arrive
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, q4 = lane & 3;

@@ -600,9 +600,9 @@ typedef struct tilemix_page_plan_args {
   int max_tokens;             /* entries of slots, >= 0 */
 } tilemix_page_plan_args;
 
-/* INVALID_ARG on a NULL pointer or a size out of range, UNSUPPORTED for a
- * page_size that is no power of two in 16 .. 1024 or too many sequences, CUDA
- * if the launch fails; all before anything is enqueued. */
+/* INVALID_ARG on a NULL pointer, a size out of range or arrays that share memory,
+ * UNSUPPORTED for a page_size that is no power of two in 16 .. 1024 or too many
+ * sequences, CUDA if the launch fails; all before anything is enqueued. */
 int tilemix_page_plan(const tilemix_page_plan_args* args, void* stream);
 
 /* Rows into the cache: token t's K and V of every KV head are coded and written
@@ -630,7 +630,8 @@ int tilemix_kv4_append(const tilemix_kv4_append_args* args, void* stream);
  * out_start[s] + position of k and v, as code * s rounded once to the cache's
  * type.  Rows outside [0, rows) are skipped and reported by tilemix_get_error()
  * as INVALID_ARG, and so are positions whose table entry names no page.  Rows
- * that no sequence covers are left as they were.  One launch. */
+ * that no sequence covers are left as they were.  k and v share no memory.  One
+ * launch. */
 typedef struct tilemix_kv4_gather_args {
   tilemix_kv4_cache cache;
   const int32_t* block_table; /* device [nseq][max_pages] */
@@ -673,7 +674,7 @@ int tilemix_kv4_gather(const tilemix_kv4_gather_args* args, void* stream);
 typedef struct tilemix_kv4_attn_args {
   tilemix_kv4_cache cache;
   const void* q;              /* device [total_q][hq][d], 16-byte aligned */
-  void* o;                    /* device out, like q */
+  void* o;                    /* device out, like q; q, o and lse share no memory */
   float* lse;                 /* device out fp32 [hq][total_q] natural-log LSE, or NULL */
   const int32_t* token_start; /* device [nseq + 1], or NULL: one query per sequence,
                                  row s (then total_q >= nseq) */

@@ -91,3 +91,56 @@ def test_the_constructor_refuses_what_the_calls_would(over):
     args.update(over)
     with pytest.raises(ValueError):
         tm.TileMixKV4Cache(**args)
+
+
+# ------------------------------------------- outputs that share memory ---
+
+BASE = 1 << 30  # addresses that are never read
+
+
+def _refused(fn, args):
+    import ctypes
+
+    import tile_routed_mixed_b200 as tm
+    assert fn(ctypes.byref(args), None) == tm.ERR_INVALID_ARG
+
+
+def test_attention_refuses_outputs_over_its_inputs():
+    """Every warp of a unit reads its rows of q, at its own time, and the first that
+    is done writes its rows of o: in place, or with o over part of q, later
+    readers would get outputs for queries."""
+    import tile_routed_mixed_b200 as tm
+    c = tm.KV4Cache(k_codes=BASE, k_scale=BASE, v_codes=BASE, v_scale=BASE, num_pages=8, page_size=16, hk=2, d=128,
+                    group=32, dtype=0)
+    size = 5 * 4 * 128 * 2  # bytes of q
+    for o, lse in ((0, None), (size - 16, None), (-size + 16, None), (size, 0), (size, size), (size, -4), (size, 2 * size - 4)):
+        a = tm.KV4AttnArgs(cache=c, q=BASE, o=BASE + o, token_start=BASE, seq_len=BASE, block_table=BASE, nseq=2,
+                           total_q=5, max_new=3, max_seqlen=64, max_pages=4, hq=4, workspace=BASE,
+                           workspace_bytes=1 << 28, sync=BASE, lse=None if lse is None else BASE + lse)
+        _refused(tm.lib().tilemix_kv4_attn, a)
+
+
+def test_gather_refuses_k_and_v_in_one_place():
+    import tile_routed_mixed_b200 as tm
+    c = tm.KV4Cache(k_codes=BASE, k_scale=BASE, v_codes=BASE, v_scale=BASE, num_pages=8, page_size=16, hk=2, d=128,
+                    group=32, dtype=0)
+    size = 9 * 2 * 128 * 2
+    for v in (0, size - 16, 16 - size):
+        _refused(tm.lib().tilemix_kv4_gather,
+                 tm.KV4GatherArgs(cache=c, block_table=BASE, seq_len=BASE, out_start=BASE, k=BASE, v=BASE + v, nseq=2,
+                                  max_pages=4, rows=9))
+
+
+def test_plan_refuses_arrays_that_share_memory():
+    """Some CTAs still read new_len when another writes granted, and so on."""
+    import itertools
+
+    import tile_routed_mixed_b200 as tm
+    names = ["token_start", "slots", "granted", "new_len", "seq_len", "block_table", "free_list", "free_count"]
+    words = dict(token_start=4, slots=4, granted=3, new_len=3, seq_len=3, block_table=12, free_list=8, free_count=1)
+    apart = {n: BASE + 256 * i for i, n in enumerate(names)}
+    for x, y in itertools.combinations(names, 2):
+        for at in (0, words[x] * 4 - 4, 4 - words[y] * 4):
+            a = tm.PagePlanArgs(nseq=3, max_pages=4, num_pages=8, page_size=16, max_tokens=4, **apart)
+            setattr(a, y, apart[x] + at)
+            _refused(tm.lib().tilemix_page_plan, a)

@@ -16,6 +16,12 @@ inline bool aligned(const void* p, uintptr_t to) {
   return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0;
 }
 
+// Whether two arrays share memory.
+inline bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + m && b < a + n;
+}
+
 // log2 of a supported page size, or -1.
 int page_shift(int page_size) {
   for (int sh = 4; sh <= 10; ++sh)
@@ -131,6 +137,23 @@ TILEMIX_API int tilemix_page_plan(const tilemix_page_plan_args* a, void* stream)
   p.num_pages = a->num_pages;
   p.page_shift = page_shift(a->page_size);
   p.max_tokens = a->max_tokens;
+  // outputs are written while inputs are still read
+  const size_t word = sizeof(int32_t), rows = word * a->nseq;
+  const struct {
+    const void* at;
+    size_t bytes;
+  } arrays[] = {{a->token_start, rows + word},
+                {a->slots, word * a->max_tokens},
+                {a->granted, rows},
+                {a->new_len, rows},
+                {a->seq_len, rows},
+                {a->block_table, rows * a->max_pages},
+                {a->free_list, word * a->num_pages},
+                {a->free_count, word}};
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (overlap(arrays[i].at, arrays[i].bytes, arrays[j].at, arrays[j].bytes))
+        return TILEMIX_ERR_INVALID_ARG;
   if (tilemix::launch_page_plan(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return TILEMIX_ERR_CUDA;
   return TILEMIX_OK;
@@ -184,6 +207,8 @@ TILEMIX_API int tilemix_kv4_gather(const tilemix_kv4_gather_args* a, void* strea
   p.nseq = a->nseq;
   p.max_pages = a->max_pages;
   p.rows = a->rows;
+  const size_t out_bytes = static_cast<size_t>(a->rows) * a->cache.hk * a->cache.d * 2;
+  if (overlap(a->k, out_bytes, a->v, out_bytes)) return TILEMIX_ERR_INVALID_ARG;
   if (tilemix::launch_kv4_gather(p, format_of(a->cache), static_cast<cudaStream_t>(stream)) !=
       cudaSuccess)
     return TILEMIX_ERR_CUDA;
@@ -230,6 +255,12 @@ TILEMIX_API int tilemix_kv4_attn(const tilemix_kv4_attn_args* a, void* stream) {
   const float scale =
       a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / std::sqrt(static_cast<float>(a->cache.d));
   p.scale_log2 = scale * 1.4426950408889634f;
+  // a unit's O is written while others still read its rows of q
+  const size_t q_bytes = static_cast<size_t>(a->total_q) * a->hq * a->cache.d * 2;
+  const size_t lse_bytes = a->lse ? static_cast<size_t>(a->total_q) * a->hq * sizeof(float) : 0;
+  if (overlap(a->q, q_bytes, a->o, q_bytes) || overlap(a->lse, lse_bytes, a->q, q_bytes) ||
+      overlap(a->lse, lse_bytes, a->o, q_bytes))
+    return TILEMIX_ERR_INVALID_ARG;
   if (tilemix::launch_kv4_attn(p, format_of(a->cache), w.shape,
                                static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return TILEMIX_ERR_CUDA;

@@ -144,3 +144,19 @@ def test_plan_refuses_arrays_that_share_memory():
             a = tm.PagePlanArgs(nseq=3, max_pages=4, num_pages=8, page_size=16, max_tokens=4, **apart)
             setattr(a, y, apart[x] + at)
             _refused(tm.lib().tilemix_page_plan, a)
+
+
+def test_the_package_imports_with_a_torch_that_has_no_cuda():
+    """The host-side entry points (routing, tile offsets, status strings) need none."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = ("import torch\n"
+            "for x in ('_cuda_getCurrentRawStream', '_cuda_getDevice', '_cuda_isCurrentStreamCapturing'):\n"
+            "    delattr(torch._C, x)\n"
+            "import tile_routed_mixed_b200 as tm\n"
+            "print(tm.tilemix_tile_offsets([0, 100, 300])[0][-1], tm.TileMixKV4Cache.__name__)\n")
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert out.returncode == 0, out.stderr
+    assert out.stdout.split() == ["3", "TileMixKV4Cache"]

@@ -33,9 +33,10 @@ class PagePlan(NamedTuple):
     granted: torch.Tensor
 
 
-_stream_of = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device index
-_device_now = torch._C._cuda_getDevice
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# (a torch without CUDA has none of these, and can make no cache)
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the current stream's handle, by device index
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 _i32 = torch.int32
 
 

@@ -58,15 +58,18 @@
 //
 // Measured (B200; from a graph of calls over three caches in turn): 64 ragged
 // sequences of up to 32768 tokens, 32/8 heads of 128, groups of 32: 1.22 GB in
-// 257 to 268 us, 4.5 to 4.7 TB/s, 0.70 to 0.72 of the measured copy rate (262 to
-// 289 us as single calls, in turn with a plain form).  The arithmetic without the
-// copies takes 241 to 246 us, the copies without the arithmetic 208 (an earlier
-// form, of eight warps): issue bounds it.  37 sequences of 16384
-// tokens: 690 instructions a tile, 0.66 of the issue slots, 0.51 of the ALU pipe,
-// 0.55 of DRAM.  Of the arithmetic, K's way to an operand costs about 23 us, V's
-// 36, the scaling and transposition of P 10, the exponentials 5, the products
-// themselves next to nothing.  8 x 4096: 18.7 us; one sequence of 65536: 29 us, of
-// 777: 10.5 us, of which 3.5 pass before the first tile is read.
+// 256 to 272 us, 4.5 to 4.8 TB/s, 0.69 to 0.73 of the measured copy rate (267 to
+// 292 us as single calls, in turn with a plain form).  What bounds it is a warp's
+// own chain from load to product, with three warps a scheduler to overlap:
+// 37 sequences of 16384 tokens take 696 instructions a tile, at full issue 174
+// cycles of the SM's four schedulers and so less than the tile's bytes, but only
+// 0.66 of the slots issue.  Of a warp's 4.5 cycles an instruction, 1 is its issue,
+// 0.96 a fixed wait for the one before, 0.89 another ready warp's turn, 0.66 and
+// 0.44 a busy pipe (ALU 0.51) or dispatch, 0.12 a load; DRAM 0.54 of nominal.  The
+// arithmetic without the copies took 241 to 246 us, of which K's way to an operand
+// is about 23, V's 36, the scaling and transposition of P 10, the exponentials 5;
+// the rest is not attributed to single steps.  8 x 4096: 19 us; one sequence of
+// 65536: 29.7 us, of 777: 10.7 us, of which 3.5 pass before the first tile is read.
 // Included by tilemix_kv4.cu.
 #pragma once
 

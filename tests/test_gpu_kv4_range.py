@@ -256,3 +256,14 @@ def test_one_key_takes_all(d, group, rep, queries, power):
                     assert (np.abs(o[i, h] - v[first, h // rep]) <=
                             (kc.EPS["bf16"] + 2.0 ** -10) * np.abs(v[first, h // rep])).all()
     assert sure > 0
+
+
+@pytest.mark.parametrize("own,later", [(-118, -76), (-89, 118), (-110, 77), (-120, 120), (-60, 122), (-40, 125)])
+@pytest.mark.parametrize("d,group,rep,queries", [(128, 64, 1, 9), (128, 64, 4, 4), (64, 32, 2, 21)])
+@pytest.mark.parametrize("length", [23, 1100])
+def test_a_later_tokens_values_far_above_tiny_ones(own, later, d, group, rep, queries, length):
+    """One huge row among the newest tokens over rows of tiny ones: neither end of
+    the type may cost the other's queries their bits."""
+    pool = kc.Pool(np.random.default_rng(12), [length], 2, d, group, 16, "bf16")
+    _fill(pool, "v", lambda at, n: np.where(at == n - (queries + 1) // 2, 2.0 ** later, 2.0 ** own))
+    _check(pool, [queries], 2 * rep)

@@ -44,8 +44,8 @@
 // scores below 2^22 and V scales within 2^-30 .. 2^40 that do not grow fourfold
 // in keys that only some columns of a unit see.  A warp that meets anything else
 // takes the unit's remaining tiles in a second, wide form of the tile: there each
-// column goes by the V scales that it sees, bf16's largest and smallest are moved
-// by a power of two, and large scores are taken against the largest before their
+// column goes by the V scales that it sees, takes bf16's largest and smallest times a
+// power of two of its own, and large scores are taken against the largest before their
 // rounding can matter.  (It costs plain calls what more code costs: 8 x 4096 19.0
 // us for 18.6, a step 49.5 for 48.1; in one form, behind branches, 18.9 and 50.6.)
 //
@@ -162,8 +162,8 @@ __device__ __forceinline__ float sum_over_rows(float x) {
 
 // Powers of two that the largest V scale takes part in a column's reference with.
 // Within kVPlain, references of any two partial states lie so near that no weight
-// is lost, and sums of V within fp32.  Beyond (bf16 only) scales are moved by
-// v_shift to where 2^95 times 2^8 times the keys of a warp, and 2^-88 less 38 bits,
+// is lost, and sums of V within fp32.  Beyond (bf16 only) scales are taken times
+// 2^-v_shift, to where 2^95 times 2^8 times the keys of a warp, and 2^-88 less 38 bits,
 // are still fp32.
 constexpr int kVPlainLow = -30, kVPlainHigh = 40;
 template <bool BF16>
@@ -186,18 +186,6 @@ __device__ __forceinline__ int v_shift(int top) {
   if (top == kVNone) return 0;
   return top > kVHigh ? top - kVHigh : min(top - kVLow<true>, 0);
 }
-// A pair of scales times 2^e (e in -121 .. 126; fp16: -11 .. 15).
-template <bool BF16>
-__device__ __forceinline__ uint32_t move2(uint32_t pair, int e) {
-  const uint32_t f = BF16 ? static_cast<uint32_t>(e + 127) << 7 : static_cast<uint32_t>(e + 15) << 10;
-  uint32_t y;
-  if constexpr (BF16)
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
-  else
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(pair), "r"(f | (f << 16)));
-  return y;
-}
-
 // What the schedule needs to know about a sequence.
 struct SeqWork {
   int len, queries, row0;  // keys, query tokens, first row of q
@@ -371,12 +359,13 @@ struct AttnTile {
   static_assert(kStages * kBytes >= 8 * NB * (D + 2) * 4, "a partial state fits a warp's ring");
 };
 
-// What a warp keeps of a unit beside its state once it is in the wide form.
+// What a warp keeps of each column beside its state once it is in the wide form.
 template <int NB>
 struct Beyond {
-  int top, shift;     // power of two of the largest V scale; what V's scales are moved by
-  bool against;       // scores are taken against raw
-  float raw[NB][2];   // the largest score of each column, before cs
+  bool against;      // scores are taken against raw
+  int power[NB][2];  // power of two of the largest V scale that the column has seen
+  int shift[NB][2];  // V's scales are taken times 2^-shift
+  float raw[NB][2];  // the largest score, before cs
 };
 
 template <int D, int GROUP, int NB, bool BF16>
@@ -849,7 +838,6 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         moved |= kWide || !(vmax < v_lim);
         if (__any_sync(0xffffffffu, moved)) {
           vmax = kv4::max_over_rows(vmax);
-          const bool parted = key0 + kAttnKeys > min_lim && min_lim < keys;
           float lg[NB][2];
           if constexpr (!kWide) {
             const int power = max(kv4::exponent(v_lim) - 1, kv4::exponent(vmax));
@@ -861,7 +849,7 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 stop |= fabsf(mx[nb][j]) >= 0x1p22f && mx[nb][j] != -INFINITY;
-            if (parted && vmax >= 2.0f * v_lim) {
+            if (key0 + kAttnKeys > min_lim && min_lim < keys && vmax >= 2.0f * v_lim) {
               // keys that not all columns see, with scales four times all that they do
               float all = 0.f;
 #pragma unroll
@@ -877,22 +865,12 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(power);
           } else {
-            constexpr int kLow = kv4::kVLow<BF16>;
             bool large = far.against;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int j = 0; j < 2; ++j) large |= fabsf(mx[nb][j]) >= 0x1p22f && mx[nb][j] != -INFINITY;
             const bool was_against = far.against, against = __any_sync(0xffffffffu, large);
-            const int top0 = far.top, shift0 = far.shift;
-            const int top = max(top0, kv4::power_of(vmax));
-            // (against: probabilities are at most one, V's scales are moved to near 2^5, or
-            // as near as one factor of the type takes them)
-            const int shift = against ? (top == kv4::kVNone ? 0 : BF16 ? max(top - 5, -126) : min(max(top - 5, -15), 11))
-                                      : BF16 ? kv4::v_shift(top) : 0;
-            const int all0 = max(top0 - shift0, kLow), all = against ? 5 : max(top - shift, kLow);
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) lg[nb][0] = lg[nb][1] = static_cast<float>(all);
             if (against) {
               // Scores, and what is there already, against the largest score (before
               // cs) first of all.
@@ -921,36 +899,31 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
                       }
                   }
                 }
-            } else if (parted) {
-              // Not all columns see all of the tile's keys: each goes by the scales that
-              // it does see, so that a later token's cost an earlier query no bits, and
-              // keeps its reference once its keys have ended.
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  float seen = 0.f;
-#pragma unroll
-                  for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                      if (key0 + 16 * mb + 8 * h + key_g < lim[nb][j]) seen = fmaxf(seen, row_scale(vsc[mb][h]));
-                  seen = kv4::max_over_rows(seen);
-                  if (lim[nb][j] <= key0)
-                    lg[nb][j] = r[nb][j] - (mv[nb][j] - 8.0f) + 5.0f;
-                  else if (lim[nb][j] < key0 + kAttnKeys)
-                    lg[nb][j] = static_cast<float>(max(max(top0, kv4::power_of(seen)) - shift, kLow));
-                }
             }
-            // the state in units of the new shift, and, where references jump, 2^64 lower
-            // (one factor could lie below fp32's range)
-            const int jump = BF16 && !against && all - all0 > 70 ? 64 : 0;
-            const float fo = kv4::two_to(min(max(shift0 - shift - jump, -126), 126)), fl = kv4::two_to(-jump);
+            // Each column goes by the V scales that it does see, so that a later token's
+            // cost an earlier query no bits.
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                l[nb][j] *= fl;
+                float seen = 0.f;
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    if (key0 + 16 * mb + 8 * h + key_g < lim[nb][j]) seen = fmaxf(seen, row_scale(vsc[mb][h]));
+                const int power = max(far.power[nb][j], kv4::power_of(kv4::max_over_rows(seen)));
+                // (against: probabilities are at most one, V's scales are taken to near 2^5)
+                const int shift = against ? (power == kv4::kVNone ? 0 : max(power - 5, -126))
+                                          : BF16 ? kv4::v_shift(power) : 0;
+                const int at0 = max(far.power[nb][j] - far.shift[nb][j], kv4::kVLow<BF16>);
+                const int at = against ? 5 : max(power - shift, kv4::kVLow<BF16>);
+                lg[nb][j] = static_cast<float>(at);
+                // the state in units of the new shift, and, where the reference jumps, 2^64
+                // lower (one factor could lie below fp32's range)
+                const int jump = BF16 && !against && at - at0 > 70 ? 64 : 0;
+                const float fo = kv4::two_to(min(max(far.shift[nb][j] - shift - jump, -126), 126));
+                l[nb][j] *= kv4::two_to(-jump);
                 r[nb][j] += static_cast<float>(jump);
 #pragma unroll
                 for (int t = 0; t < kT; ++t)
@@ -959,14 +932,9 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
                     o[t][i][nb][j] *= fo;
                     o[t][i][nb][2 + j] *= fo;
                   }
+                far.power[nb][j] = power, far.shift[nb][j] = shift;
               }
-#pragma unroll
-            for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < (kNg + 1) / 2; ++i) vsc[mb][h][i] = kv4::move2<BF16>(vsc[mb][h][i], -shift);
-            far.top = top, far.shift = shift, far.against = against;
+            far.against = against;
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
@@ -990,6 +958,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         }
 
         // P and P V
+        const auto scale_for = [&](float f, int nb, int j) {
+          if constexpr (!kWide) return f;
+          const float x = f * kv4::two_to(-far.shift[nb][j]);
+          return x > 0x1p126f ? 0x1p126f : x;  // (finite where the column does not see it: 0 x)
+        };
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
 #pragma unroll
@@ -1018,8 +991,11 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
             uint32_t pb[NB][2];
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
-              pb[nb][0] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][0] * f0, s[mb][nb][1] * f0));
-              pb[nb][1] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][2] * f1, s[mb][nb][3] * f1));
+              // (in the wide form each column takes V's scales its own way)
+              const float f00 = scale_for(f0, nb, 0), f01 = scale_for(f0, nb, 1);
+              const float f10 = scale_for(f1, nb, 0), f11 = scale_for(f1, nb, 1);
+              pb[nb][0] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][0] * f00, s[mb][nb][1] * f01));
+              pb[nb][1] = kv4::transpose8x8(kv4::pack2<false>(s[mb][nb][2] * f10, s[mb][nb][3] * f11));
             }
 #pragma unroll
             for (int t = i * kTg; t < (i + 1) * kTg; ++t) {
@@ -1053,9 +1029,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
         wide = key0 < keys && !tile(std::false_type(), key0);
       }
       if (wide) {
-        far.top = v_lim == kv4::kVStart ? kv4::kVNone : kv4::exponent(v_lim) - 1;
-        far.shift = 0;
         far.against = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            far.power[nb][j] = v_lim == kv4::kVStart ? kv4::kVNone : kv4::exponent(v_lim) - 1;
+            far.shift[nb][j] = 0;
+          }
 #pragma unroll 1
         for (;;) {
           const int key0 = (t0 + it) * kAttnKeys;
@@ -1085,13 +1066,14 @@ __global__ void __launch_bounds__(32 * kAttnWarps<NB>, 1)
           for (int j = 0; j < 2; ++j) {
             // the power in the column's reference
             int lg = mv[nb][j] == -INFINITY ? 0 : __float2int_rn(r[nb][j] - mv[nb][j] + 13.0f);
-            int unit = min(max(lg + far.shift, kv4::kVPlainLow), kv4::kVPlainHigh);
+            const int shift = far.shift[nb][j];
+            int unit = min(max(lg + shift, kv4::kVPlainLow), kv4::kVPlainHigh);
             if (far.against) {
               // (the same for all, so that equal scores of two states weigh the same)
-              lg = 5, unit = far.shift > 80 ? kv4::kVPlainHigh : 5;
+              lg = 5, unit = shift > 80 ? kv4::kVPlainHigh : 5;
               r[nb][j] = far.raw[nb][j] * cs[nb][j];
             }
-            const float to_o = kv4::two_to(lg + far.shift - unit), to_l = kv4::two_to(lg - unit);
+            const float to_o = kv4::two_to(lg + shift - unit), to_l = kv4::two_to(lg - unit);
             l[nb][j] *= to_l;
             r[nb][j] += static_cast<float>(unit - lg);
 #pragma unroll

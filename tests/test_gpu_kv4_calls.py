@@ -201,3 +201,32 @@ def test_a_shared_prefix_ends_as_documented():
     step([-38, 0, 1])             # the first ends and returns them
     assert set(shared) <= set(cache.free_list[:int(cache.free_count)].tolist())
     step([16, 0, 1])
+
+
+# ------------------------------------------------------------------ size ---
+
+def test_a_pool_beyond_four_gigabytes():
+    """Rows on both sides of the byte offset 2^32 in a pool of 4.7 GB for each of K and
+    V: appended, attended to and read back."""
+    import tile_routed_mixed_b200 as tm
+    rng = np.random.default_rng(44)
+    hq, hk, d, page, group, n = 8, 8, 128, 1024, 32, 2300
+    cache = tm.TileMixKV4Cache(9000, page, hk, d, 2, 4, group=group, dtype=torch.bfloat16)
+    edge = 2 ** 32 // (page * hk * d // 2)             # the page that starts at 2^32
+    table = [[edge, 8999, edge - 1, -1], [1, edge + 1, -1, -1]]
+    lengths = [n, 1100]
+    cache.block_table.copy_(torch.tensor(table, dtype=torch.int32))
+    cache.seq_len.copy_(torch.tensor(lengths, dtype=torch.int32))
+    slots = np.concatenate([np.array(table[s])[np.arange(m) // page] * page + np.arange(m) % page
+                            for s, m in enumerate(lengths)])
+    k, v = (kc.draw(rng, (sum(lengths), hk, d), "bf16") for _ in range(2))
+    cache.append(kc.to_device(k, "bf16"), kc.to_device(v, "bf16"), _i32(slots))
+    coded = [okv.values(*okv.quantise(x, group, "bf16"), group) for x in (k, v)]
+    got = cache.gather(_i32([0, n]), sum(lengths))
+    for t, x in zip(got, coded):
+        assert np.array_equal(kc.to_numpy(t), okv.round_to(x, "bf16"))
+    q = kc.draw(rng, (3, hq, d), "bf16")
+    o, lse = cache.attend(kc.to_device(q, "bf16"), n, token_start=_i32([0, 2, 3]), max_new=2, lse=True)
+    pool = type("P", (), {"dtype": "bf16"})
+    kc.check_attend(kc.to_numpy(o), kc.to_numpy(lse), q, pool, lengths, [0, 2, 3], hq,
+                    kv=lambda s: [x[n * s:n * s + lengths[s]] for x in coded])

@@ -64,8 +64,8 @@
 // 37 sequences of 16384 tokens take 696 instructions a tile, at full issue 174
 // cycles of the SM's four schedulers and so less than the tile's bytes, but only
 // 0.66 of the slots issue.  Of a warp's 4.5 cycles an instruction, 1 is its issue,
-// 0.96 a fixed wait for the one before, 0.89 another ready warp's turn, 0.66 and
-// 0.44 a busy pipe (ALU 0.51) or dispatch, 0.12 a load; DRAM 0.54 of nominal.  The
+// 0.97 a fixed wait for the one before, 0.88 another ready warp's turn, 0.65 and
+// 0.43 a busy pipe (ALU 0.51) or dispatch, 0.12 a load; DRAM 0.54 of nominal.  The
 // arithmetic without the copies took 241 to 246 us, of which K's way to an operand
 // is about 23, V's 36, the scaling and transposition of P 10, the exponentials 5;
 // the rest is not attributed to single steps.  8 x 4096: 19 us; one sequence of
